@@ -296,6 +296,89 @@ moe_status moe_quantize_act(const moe_layer_desc* desc, const uint16_t* x_bf16, 
 moe_status moe_pack_scales(int32_t rows, int32_t groups, const uint8_t* sf, int32_t* packed, void* stream);
 moe_status moe_unpack_scales(int32_t rows, int32_t groups, const int32_t* packed, uint8_t* sf, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Tokens in expert order and back, with gradients.
+ *
+ * The parts of the layer around its experts, for callers that run the experts themselves (a
+ * training step, another expert body, weights in other formats) or bring a router of their
+ * own: sort the (token, slot) pairs by expert, gather the tokens into expert order, bring the
+ * experts' rows back with the routing weights, and the gradients of both.
+ *
+ * With r(t, j) = slot_to_row[t*k + j], and "has a row" meaning 0 <= r(t, j) < max_rows:
+ *   moe_dispatch            xs[r(t, j)]  = x[t]                        for every slot with a row
+ *   moe_dispatch_backward   dx[t]        = sum_j dxs[r(t, j)]           (0 without a row)
+ *   moe_combine             y[t]         = sum_j w[t, j] * ys[r(t, j)]  (0 without a row)
+ *   moe_combine_backward    dys[r(t, j)] = w[t, j] * dy[t]
+ *                           dw[t, j]     = <dy[t], ys[r(t, j)]>         (0 without a row)
+ *                           dlogits[t,e] = sum over j with topk_ids[t, j] = e of
+ *                                          w[t, j] * (dw[t, j] - sum_i w[t, i] * dw[t, i])
+ * dlogits is the gradient of the routing logits where w is the softmax over the k chosen ones
+ * (moe_route_permute).  It is linear in dw: on one GPU's share of the experts it is that share's
+ * part, and the parts of all shares add up.
+ *
+ *   - x, dx, y and dy are in token order: T rows of H elements, token_stride elements apart.
+ *     xs, dxs, ys and dys are in expert order: max_rows rows, row_stride elements apart.  All are
+ *     of the descriptor's dtype (MOE_DT_U8: bytes, moe_dispatch only: packed codes, scales).
+ *     topk_w, dw [T, k] and dlogits [T, E_tot] are float32 and dense, topk_ids int32 [T, k].
+ *   - Sums are taken in float32 in slot order and rounded once (to nearest even) to the dtype;
+ *     there are no atomics, so results are the same from run to run.  A slot without a row is
+ *     left out (its weight is not read as 0 times something); a row with a weight of 0 is read.
+ *   - Rows that no slot owns, and the elements between H and the stride, are left as they were.
+ *   - slot_to_row comes from moe_sort_tokens or moe_route_permute; a map entry outside
+ *     [0, max_rows) counts as no row, so rows past the caller's tensors are dropped.  Two slots
+ *     with one row (not something the sort makes) give that row from either.
+ *   - Pointers are aligned to their element; outputs must not overlap inputs or each other.
+ *     Stream, validation and error rules are those at the top of this file.  num_tokens = 0
+ *     launches nothing.
+ *   - Limits: 1 <= H <= 2^20; 1 <= E_loc <= E_tot <= 1024; 1 <= k <= 16; T*k < 2^31; strides
+ *     0 (= H) or H to 2^40; max_rows 0 (= T*k) to T*k. */
+
+/* Element types of the tensors below. */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1, MOE_DT_F32 = 2, MOE_DT_U8 = 3 } moe_dtype;
+
+typedef struct {
+  int32_t num_tokens;    /* T >= 0 */
+  int32_t hidden;        /* H */
+  int32_t num_experts;   /* E_tot */
+  int32_t local_begin;   /* e0: local experts are [e0, e0 + E_loc) */
+  int32_t num_local;     /* E_loc */
+  int32_t topk;          /* k slots per token; a token may name an expert more than once */
+  int32_t dtype;         /* moe_dtype */
+  int32_t max_rows;      /* rows the expert-ordered tensors hold; 0 = T*k */
+  int64_t token_stride;  /* elements between token rows; 0 = H */
+  int64_t row_stride;    /* elements between expert-ordered rows; 0 = H */
+} moe_dispatch_desc;
+
+/* Bytes of workspace moe_sort_tokens needs.  Host only; validates the descriptor. */
+moe_status moe_sort_workspace_size(const moe_dispatch_desc* desc, size_t* bytes);
+
+/* Group the (token, slot) pairs by local expert, stable by slot id, from expert ids of any
+ * router: counts, offsets, row_to_slot and slot_to_row as moe_route_permute writes them (same
+ * sizes and meaning).  An id outside the local experts, negative ones among them, is not local.
+ * hidden, dtype, max_rows and the strides are not used (they must be valid). */
+moe_status moe_sort_tokens(const moe_dispatch_desc* desc, const int32_t* topk_ids, int32_t* counts, int32_t* offsets,
+                           int32_t* row_to_slot, int32_t* slot_to_row, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Gather: xs[r(t, j)] = x[t].  Reads each token that has a row once. */
+moe_status moe_dispatch(const moe_dispatch_desc* desc, const void* x, const int32_t* slot_to_row, void* xs,
+                        void* stream);
+
+/* Gradient of moe_dispatch: dx[t] = sum_j dxs[r(t, j)].  Writes every dx row. */
+moe_status moe_dispatch_backward(const moe_dispatch_desc* desc, const void* dxs, const int32_t* slot_to_row, void* dx,
+                                 void* stream);
+
+/* Weighted sum back into token order: y[t] = sum_j w[t, j] * ys[r(t, j)].  Writes every y row. */
+moe_status moe_combine(const moe_dispatch_desc* desc, const void* ys, const int32_t* slot_to_row, const float* topk_w,
+                       void* y, void* stream);
+
+/* Gradients of moe_combine: dys and dw, and the router's dlogits unless opt_dlogits is NULL
+ * (topk_ids is then not read and may be NULL).  Writes dys on the rows slots own, all of dw and
+ * all of dlogits. */
+moe_status moe_combine_backward(const moe_dispatch_desc* desc, const void* dy, const void* ys,
+                                const int32_t* slot_to_row, const float* topk_w, void* dys, float* dw,
+                                const int32_t* topk_ids, float* opt_dlogits, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

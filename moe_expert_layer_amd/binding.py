@@ -38,6 +38,19 @@ class MoeLayerDesc(ctypes.Structure):
     ]
 
 
+MOE_DT_BF16, MOE_DT_F16, MOE_DT_F32, MOE_DT_U8 = range(4)
+DTYPES = {"bf16": MOE_DT_BF16, "f16": MOE_DT_F16, "f32": MOE_DT_F32, "u8": MOE_DT_U8}
+
+
+class MoeDispatchDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int32), ("hidden", ctypes.c_int32), ("num_experts", ctypes.c_int32),
+        ("local_begin", ctypes.c_int32), ("num_local", ctypes.c_int32), ("topk", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("max_rows", ctypes.c_int32), ("token_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+    ]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{status_str(status)}: {msg}")
@@ -82,6 +95,17 @@ def lib():
         L.moe_pack_scales.argtypes = [I32, I32, P, P, VP]
         L.moe_unpack_scales.restype = I32
         L.moe_unpack_scales.argtypes = [I32, I32, P, P, VP]
+        DD = ctypes.POINTER(MoeDispatchDesc)
+        for name, args in {
+            "moe_sort_workspace_size": [DD, ctypes.POINTER(ctypes.c_size_t)],
+            "moe_sort_tokens": [DD, P, P, P, P, P, P, S, VP],
+            "moe_dispatch": [DD, P, P, P, VP],
+            "moe_dispatch_backward": [DD, P, P, P, VP],
+            "moe_combine": [DD, P, P, P, P, VP],
+            "moe_combine_backward": [DD, P, P, P, P, P, P, P, P, VP],
+        }.items():
+            f = getattr(L, name)
+            f.restype, f.argtypes = I32, args
         _lib = L
     return _lib
 
@@ -203,3 +227,170 @@ def alloc_workspace(desc, device="cuda"):
     """A uint8 device tensor of moe_workspace_size(desc) bytes (torch allocations are 256-byte aligned)."""
     import torch
     return torch.empty(max(moe_workspace_size(desc), 256), dtype=torch.uint8, device=device)
+
+
+# ---------------------------------------------------------------------------------------
+# operators beside the layer.  Their tensors carry their sizes, so these functions also check them
+# against the descriptor (dtype, shape, row stride, device) before they hand out pointers, and run on
+# the tensors' device whichever device is current.
+
+def _refuse(status: int, msg: str):
+    raise MoeError(status, msg)
+
+
+def _rows_tensor(name, t, dtype, rows, cols, stride, dev, at_least=False):
+    """A [rows, cols] tensor of dtype on device dev whose rows lie stride elements apart (at_least: it
+    may have more rows)."""
+    if t.dtype is not dtype:
+        _refuse(MOE_ERR_INVALID_DESC, f"{name} is {t.dtype}, not {dtype}")
+    if t.get_device() != dev:
+        _refuse(MOE_ERR_UNSUPPORTED, f"{name} is not on the GPU of the other tensors")
+    sh, st = t.shape, t.stride()
+    if len(sh) != 2 or sh[1] != cols or (sh[0] < rows if at_least else sh[0] != rows):
+        _refuse(MOE_ERR_INVALID_DESC, f"{name} has shape {tuple(sh)}, not ({rows}, {cols})")
+    if (st[1] != 1 and cols > 1) or (st[0] != stride and rows > 1):
+        _refuse(MOE_ERR_INVALID_DESC, f"{name} has strides {st}, not ({stride}, 1)")
+
+
+def _array(name, t, dtype, n, dev):
+    """A dense tensor of dtype with at least n elements on device dev."""
+    if t.dtype is not dtype:
+        _refuse(MOE_ERR_INVALID_DESC, f"{name} is {t.dtype}, not {dtype}")
+    if t.get_device() != dev:
+        _refuse(MOE_ERR_UNSUPPORTED, f"{name} is not on the GPU of the other tensors")
+    if t.numel() < n or not t.is_contiguous():
+        _refuse(MOE_ERR_INVALID_DESC, f"{name} holds {t.numel()} elements (contiguous: {t.is_contiguous()}), needs {n}")
+
+
+def _device_of(t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        _refuse(MOE_ERR_UNSUPPORTED, "tensors must be on a GPU")
+    return dev
+
+
+def _launch(fn, dev: int, stream, *args):
+    """fn(*args, stream) with device dev current, on its current stream unless one is given."""
+    import torch
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device.index != dev:
+            _refuse(MOE_ERR_UNSUPPORTED, f"stream of GPU {stream.device.index}, tensors on GPU {dev}")
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        _check(fn(*args, raw))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, raw))
+
+
+_TORCH_DTYPES = None
+
+
+def _torch_dtype(dtype: int):
+    global _TORCH_DTYPES
+    if _TORCH_DTYPES is None:
+        import torch
+        _TORCH_DTYPES = {MOE_DT_BF16: torch.bfloat16, MOE_DT_F16: torch.float16, MOE_DT_F32: torch.float32,
+                         MOE_DT_U8: torch.uint8}
+    if dtype not in _TORCH_DTYPES:
+        _refuse(MOE_ERR_INVALID_DESC, f"dtype {dtype} unknown")
+    return _TORCH_DTYPES[dtype]
+
+
+def make_dispatch_desc(num_tokens: int, hidden: int, num_experts: int, topk: int, local_begin: int = 0,
+                       num_local: Optional[int] = None, dtype: str = "bf16", max_rows: int = 0, token_stride: int = 0,
+                       row_stride: int = 0) -> MoeDispatchDesc:
+    """Descriptor of tokens in expert order.  dtype: "bf16", "f16", "f32" or "u8" (bytes, moe_dispatch only);
+    max_rows: rows of the expert-ordered tensors (0 = num_tokens * topk); strides in elements (0 = hidden)."""
+    return MoeDispatchDesc(num_tokens, hidden, num_experts, local_begin,
+                           num_experts - local_begin if num_local is None else num_local, topk, DTYPES[dtype],
+                           max_rows, token_stride, row_stride)
+
+
+def moe_sort_workspace_size(desc: MoeDispatchDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_sort_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_sort_workspace(desc: MoeDispatchDesc, device="cuda"):
+    """A uint8 device tensor of moe_sort_workspace_size(desc) bytes."""
+    import torch
+    return torch.empty(max(moe_sort_workspace_size(desc), 256), dtype=torch.uint8, device=device)
+
+
+def _token_tensor(name, d, t, dev):
+    _rows_tensor(name, t, _torch_dtype(d.dtype), d.num_tokens, d.hidden, d.token_stride or d.hidden, dev)
+
+
+def _expert_tensor(name, d, t, dev):
+    _rows_tensor(name, t, _torch_dtype(d.dtype), d.max_rows or d.num_tokens * d.topk, d.hidden,
+                 d.row_stride or d.hidden, dev, at_least=True)
+
+
+def moe_sort_tokens(desc, topk_ids, counts, offsets, row_to_slot, slot_to_row, workspace, stream=None):
+    """Expert ids int32 [T, k] -> counts, offsets, row_to_slot, slot_to_row (int32), as moe_route_permute writes them."""
+    import torch
+    dev, n, i32 = _device_of(topk_ids), desc.num_tokens * desc.topk, torch.int32
+    _array("topk_ids", topk_ids, i32, n, dev)
+    _array("counts", counts, i32, desc.num_local, dev)
+    _array("offsets", offsets, i32, desc.num_local + 1, dev)
+    _array("row_to_slot", row_to_slot, i32, n, dev)
+    _array("slot_to_row", slot_to_row, i32, n, dev)
+    _array("workspace", workspace, torch.uint8, 0, dev)
+    _launch(lib().moe_sort_tokens, dev, stream, ctypes.byref(desc), topk_ids.data_ptr(), counts.data_ptr(),
+            offsets.data_ptr(), row_to_slot.data_ptr(), slot_to_row.data_ptr(), workspace.data_ptr(), workspace.numel())
+
+
+def moe_dispatch(desc, x, slot_to_row, xs, stream=None):
+    """Token rows x [T, H] -> expert-ordered rows xs [max_rows, H] (rows that no slot owns are left as they were)."""
+    import torch
+    dev = _device_of(x)
+    _token_tensor("x", desc, x, dev)
+    _array("slot_to_row", slot_to_row, torch.int32, desc.num_tokens * desc.topk, dev)
+    _expert_tensor("xs", desc, xs, dev)
+    _launch(lib().moe_dispatch, dev, stream, ctypes.byref(desc), x.data_ptr(), slot_to_row.data_ptr(), xs.data_ptr())
+
+
+def moe_dispatch_backward(desc, dxs, slot_to_row, dx, stream=None):
+    """Gradient of moe_dispatch: dx[t] = the sum of the rows of dxs that token t went to."""
+    import torch
+    dev = _device_of(dxs)
+    _expert_tensor("dxs", desc, dxs, dev)
+    _array("slot_to_row", slot_to_row, torch.int32, desc.num_tokens * desc.topk, dev)
+    _token_tensor("dx", desc, dx, dev)
+    _launch(lib().moe_dispatch_backward, dev, stream, ctypes.byref(desc), dxs.data_ptr(), slot_to_row.data_ptr(),
+            dx.data_ptr())
+
+
+def moe_combine(desc, ys, slot_to_row, topk_w, y, stream=None):
+    """Expert-ordered rows ys -> y[t] = sum_j topk_w[t, j] * ys[slot_to_row[t, j]], in token order."""
+    import torch
+    dev, n = _device_of(ys), desc.num_tokens * desc.topk
+    _expert_tensor("ys", desc, ys, dev)
+    _array("slot_to_row", slot_to_row, torch.int32, n, dev)
+    _array("topk_w", topk_w, torch.float32, n, dev)
+    _token_tensor("y", desc, y, dev)
+    _launch(lib().moe_combine, dev, stream, ctypes.byref(desc), ys.data_ptr(), slot_to_row.data_ptr(),
+            topk_w.data_ptr(), y.data_ptr())
+
+
+def moe_combine_backward(desc, dy, ys, slot_to_row, topk_w, dys, dw, topk_ids=None, dlogits=None, stream=None):
+    """Gradients of moe_combine: dys (rows), dw [T, k] float32 and, where dlogits [T, E_tot] float32 is given
+    (with topk_ids), the gradient of the routing logits under the softmax over the chosen ones."""
+    import torch
+    dev, n = _device_of(dy), desc.num_tokens * desc.topk
+    _token_tensor("dy", desc, dy, dev)
+    _expert_tensor("ys", desc, ys, dev)
+    _array("slot_to_row", slot_to_row, torch.int32, n, dev)
+    _array("topk_w", topk_w, torch.float32, n, dev)
+    _expert_tensor("dys", desc, dys, dev)
+    _array("dw", dw, torch.float32, n, dev)
+    if topk_ids is not None:
+        _array("topk_ids", topk_ids, torch.int32, n, dev)
+    if dlogits is not None:
+        _array("dlogits", dlogits, torch.float32, desc.num_tokens * desc.num_experts, dev)
+    _launch(lib().moe_combine_backward, dev, stream, ctypes.byref(desc), dy.data_ptr(), ys.data_ptr(),
+            slot_to_row.data_ptr(), topk_w.data_ptr(), dys.data_ptr(), dw.data_ptr(), _ptr(topk_ids), _ptr(dlogits))

@@ -1,0 +1,348 @@
+// Tokens sorted by expert and brought back with their routing weights, and both gradients.
+//
+// With r(t, j) = slot_to_row[t k + j], the row of slot j of token t (none when the slot's expert is
+// not local, or its row lies at or past the rows the caller's tensors hold):
+//   dispatch           xs[r(t, j)] = x[t]
+//   dispatch backward  dx[t]       = sum_j dxs[r(t, j)]
+//   combine            y[t]        = sum_j w[t, j] ys[r(t, j)]
+//   combine backward   dys[r(t, j)] = w[t, j] dy[t],   dw[t, j] = <dy[t], ys[r(t, j)]> (0: no row)
+//                      dlogits[t, e] = sum over j with ids[t, j] = e of w_j (dw_j - sum_i w_i dw_i)
+// Every sum is taken in float32 in slot order (the dot products: per lane, then over lanes, then over
+// waves, all in a fixed order) and rounded once to the tensors' type; every output element has one
+// writer, so results do not depend on scheduling.
+//
+// All four move rows and do next to no arithmetic: what bounds them is HBM (large calls) or the
+// latency of one chain map -> row -> store (small ones).  A workgroup takes one token at a time: the
+// first k lanes of every wave load its map entries in one instruction, a ballot compacts the slots
+// that have a row, and the row loads are issued before any of them is used.
+#include <hip/hip_runtime.h>
+#include <hip/hip_fp16.h>
+#include <cstdint>
+
+#include "device_common.hpp"
+#include "moe_internal.hpp"
+
+namespace moe {
+
+// 16 bytes of a row at the alignment of its elements: the hardware takes any alignment, the type
+// tells the compiler not to assume 16 bytes (odd row lengths and strides)
+template <int A>
+struct alignas(A) Chunk16 { uint32_t w[4]; };
+template <>
+struct __attribute__((packed)) Chunk16<1> { uint32_t w[4]; };
+template <>
+struct __attribute__((packed, aligned(2))) Chunk16<2> { uint32_t w[4]; };
+
+struct Bf16 { uint16_t b; };
+struct F16 { uint16_t b; };
+
+template <typename T> struct Elem;
+template <> struct Elem<Bf16> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ float get(Bf16 v) { return __uint_as_float((uint32_t)v.b << 16); }
+  static __device__ __forceinline__ Bf16 put(float f) {
+    return Bf16{__builtin_bit_cast(uint16_t, (__bf16)f)};  // round to nearest even
+  }
+  static __device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Elem<F16> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ float get(F16 v) { return (float)__builtin_bit_cast(_Float16, v.b); }
+  static __device__ __forceinline__ F16 put(float f) { return F16{__builtin_bit_cast(uint16_t, (_Float16)f)}; }
+  static __device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = get(F16{(uint16_t)(w[i] & 0xffffu)});
+      f[2 * i + 1] = get(F16{(uint16_t)(w[i] >> 16)});
+    }
+  }
+};
+template <> struct Elem<float> {
+  static constexpr int kVec = 4;
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float f) { return f; }
+  static __device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void pack16(const float (&f)[Elem<T>::kVec], uint32_t (&w)[4]) {
+  T v[Elem<T>::kVec];
+#pragma unroll
+  for (int i = 0; i < Elem<T>::kVec; ++i) v[i] = Elem<T>::put(f[i]);
+  __builtin_memcpy(w, v, 16);
+}
+
+// The rows of token t's slots, in lane j's register for slot j < k (any wave); the mask has bit j
+// set when slot j has a row below max_rows (a map entry outside [0, max_rows) counts as none).
+__device__ __forceinline__ uint64_t token_rows(const int32_t* __restrict__ s2r, long long t, int k, int max_rows,
+                                               int lane, int& row) {
+  row = lane < k ? s2r[t * k + lane] : -1;
+  return __ballot((unsigned)row < (unsigned)max_rows);
+}
+
+// grid (column chunks, tokens): 256 threads, kDispatchPer 16-byte chunks of the token's row each
+constexpr int kDispatchPer = 2;
+
+__global__ __launch_bounds__(256) void dispatch_kernel(const uint8_t* __restrict__ x, long long x_pitch,
+                                                       const int32_t* __restrict__ s2r, int T, int k, int max_rows,
+                                                       long long row_bytes, uint8_t* __restrict__ xs,
+                                                       long long xs_pitch) {
+  const int lane = threadIdx.x & 63;
+  const long long c0 = ((long long)blockIdx.x * (256 * kDispatchPer) + threadIdx.x) * 16;
+  for (int t = blockIdx.y; t < T; t += gridDim.y) {
+    int row;
+    uint64_t mask = token_rows(s2r, t, k, max_rows, lane, row);
+    if (mask == 0) continue;
+    const uint8_t* src = x + (long long)t * x_pitch;
+    Chunk16<1> v[kDispatchPer];
+#pragma unroll
+    for (int i = 0; i < kDispatchPer; ++i) {
+      const long long c = c0 + i * 4096;
+      if (c + 16 <= row_bytes) v[i] = *reinterpret_cast<const Chunk16<1>*>(src + c);
+    }
+    while (mask) {
+      const int j = __builtin_ctzll(mask);
+      mask &= mask - 1;
+      uint8_t* dst = xs + (long long)__builtin_amdgcn_readlane(row, j) * xs_pitch;
+#pragma unroll
+      for (int i = 0; i < kDispatchPer; ++i) {
+        const long long c = c0 + i * 4096;
+        if (c + 16 <= row_bytes) *reinterpret_cast<Chunk16<1>*>(dst + c) = v[i];
+        else
+          for (long long b = c; b < row_bytes; ++b) dst[b] = src[b];  // the row's last, partial chunk
+      }
+    }
+  }
+}
+
+// y[t] = sum over the token's rows of weight * row (WEIGHTED) or of the rows themselves.
+// grid (column chunks, tokens): 256 threads, one 16-byte chunk each; the rows are taken four at a
+// time, their loads issued before the sum.
+template <typename T, bool WEIGHTED>
+__global__ __launch_bounds__(256) void combine_rows_kernel(const T* __restrict__ ys, long long ys_stride,
+                                                           const int32_t* __restrict__ s2r,
+                                                           const float* __restrict__ w, int ntok, int k, int max_rows,
+                                                           int H, T* __restrict__ y, long long y_stride) {
+  constexpr int V = Elem<T>::kVec;
+  using C = Chunk16<sizeof(T)>;
+  const int lane = threadIdx.x & 63;
+  const int c = (blockIdx.x * 256 + threadIdx.x) * V;
+  const bool whole = c + V <= H;
+  for (int t = blockIdx.y; t < ntok; t += gridDim.y) {
+    int row;
+    uint64_t mask = token_rows(s2r, t, k, max_rows, lane, row);
+    const float wl = WEIGHTED && lane < k ? w[(long long)t * k + lane] : 1.f;
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    while (mask) {
+      const T* src[4];
+      float wt[4];
+      int n = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (mask) {
+          const int j = __builtin_ctzll(mask);
+          mask &= mask - 1;
+          src[q] = ys + (long long)__builtin_amdgcn_readlane(row, j) * ys_stride + c;
+          wt[q] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wl), j));
+          n = q + 1;
+        }
+      if (whole) {
+        C v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < n) v[q] = *reinterpret_cast<const C*>(src[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < n) {
+            float f[V];
+            Elem<T>::unpack(v[q].w, f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = WEIGHTED ? fmaf(wt[q], f[i], acc[i]) : acc[i] + f[i];
+          }
+      } else if (c < H) {
+        for (int q = 0; q < n; ++q)
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (c + i < H) {
+              const float f = Elem<T>::get(src[q][i]);
+              acc[i] = WEIGHTED ? fmaf(wt[q], f, acc[i]) : acc[i] + f;
+            }
+      }
+    }
+    T* dst = y + (long long)t * y_stride + c;
+    if (whole) {
+      C o;
+      pack16<T>(acc, o.w);
+      *reinterpret_cast<C*>(dst) = o;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (c + i < H) dst[i] = Elem<T>::put(acc[i]);
+    }
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+
+// One workgroup (NW waves) per token.  With n rows the waves split into n groups of P = NW / n: each
+// group takes one row, each of its waves every P-th 64-chunk piece of it, so the work is spread
+// whether a token has one local row or all k of them.  (n > NW: the waves take the rows in turn.)
+template <typename T, int NW>
+__global__ __launch_bounds__(NW * 64) void combine_backward_kernel(
+    const T* __restrict__ dy, long long dy_stride, const T* __restrict__ ys, long long row_stride,
+    const int32_t* __restrict__ s2r, const float* __restrict__ w, int ntok, int k, int max_rows, int H,
+    T* __restrict__ dys, float* __restrict__ dw, const int32_t* __restrict__ ids, int E, float* __restrict__ dlogits) {
+  constexpr int V = Elem<T>::kVec, U = 4;  // chunks in flight per lane
+  using C = Chunk16<sizeof(T)>;
+  __shared__ float part[16][NW];  // [slot][wave of its group]
+  __shared__ float g[16];
+  __shared__ int gid[16];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nchunk = H / V;  // whole 16-byte chunks of a row
+  for (int t = blockIdx.x; t < ntok; t += gridDim.x) {
+    int row;
+    const uint64_t mask = token_rows(s2r, t, k, max_rows, lane, row);
+    const float wl = lane < k ? w[(long long)t * k + lane] : 0.f;
+    const int n = __popcll(mask);
+    const int P = n == 0 ? 1 : n < NW ? NW / n : 1;
+    const T* dyt = dy + (long long)t * dy_stride;
+    for (int q = wave / P; q < n; q += NW / P) {  // q-th slot with a row; one pass unless n > NW
+      uint64_t m = mask;
+      for (int i = 0; i < q; ++i) m &= m - 1;
+      const int j = __builtin_ctzll(m), p = wave % P;
+      const long long r = __builtin_amdgcn_readlane(row, j);
+      const float wt = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wl), j));
+      const T* src = ys + r * row_stride;
+      T* dst = dys + r * row_stride;
+      float dot = 0.f;
+      for (int c0 = p * 64 + lane; c0 < nchunk; c0 += P * 64 * U) {
+        C a[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int c = c0 + u * P * 64;
+          if (c < nchunk) {
+            a[u] = *reinterpret_cast<const C*>(dyt + (long long)c * V);
+            b[u] = *reinterpret_cast<const C*>(src + (long long)c * V);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int c = c0 + u * P * 64;
+          if (c < nchunk) {
+            float fa[V], fb[V], o[V];
+            Elem<T>::unpack(a[u].w, fa);
+            Elem<T>::unpack(b[u].w, fb);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              dot = fmaf(fa[i], fb[i], dot);
+              o[i] = wt * fa[i];
+            }
+            C ov;
+            pack16<T>(o, ov.w);
+            *reinterpret_cast<C*>(dst + (long long)c * V) = ov;
+          }
+        }
+      }
+      if (p == 0) {  // the elements after the last whole chunk
+        const int c = nchunk * V + lane;
+        if (c < H) {
+          const float fa = Elem<T>::get(dyt[c]);
+          dot = fmaf(fa, Elem<T>::get(src[c]), dot);
+          dst[c] = Elem<T>::put(wt * fa);
+        }
+      }
+      dot = wave_sum(dot);
+      if (lane == 0) part[j][p] = dot;
+    }
+    __syncthreads();
+    if (wave == 0) {
+      float d = 0.f;
+      if (lane < k && ((mask >> lane) & 1))
+        for (int p = 0; p < P; ++p) d += part[lane][p];
+      if (lane < k) dw[(long long)t * k + lane] = d;
+      if (dlogits != nullptr) {
+        float s = 0.f;  // sum_i w_i dw_i in slot order
+        for (int i = 0; i < k; ++i)
+          s = fmaf(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wl), i)),
+                   __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(d), i)), s);
+        if (lane < k) {
+          g[lane] = wl * (d - s);
+          gid[lane] = ids[(long long)t * k + lane];
+        }
+      }
+    }
+    __syncthreads();
+    if (dlogits != nullptr)
+      for (int e = threadIdx.x; e < E; e += NW * 64) {
+        float v = 0.f;
+        for (int i = 0; i < k; ++i) v += gid[i] == e ? g[i] : 0.f;
+        dlogits[(long long)t * E + e] = v;
+      }
+    // part, g and gid are rewritten only after the next token's barriers: part before the first
+    // (its readers, wave 0, are past the second), g and gid between them
+    __syncthreads();
+  }
+}
+
+static unsigned token_grid(int T) { return (unsigned)(T < 65535 ? T : 65535); }
+
+hipError_t launch_dispatch(const DispatchShape& d, const void* x, const int32_t* s2r, void* xs, hipStream_t s) {
+  const long long es = dtype_bytes(d.dtype), row_bytes = (long long)d.H * es;
+  const unsigned chunks = (unsigned)((row_bytes + 4096 * kDispatchPer - 1) / (4096 * kDispatchPer));
+  dispatch_kernel<<<dim3(chunks, token_grid(d.T)), 256, 0, s>>>(
+      static_cast<const uint8_t*>(x), d.token_stride * es, s2r, d.T, d.k, d.max_rows, row_bytes,
+      static_cast<uint8_t*>(xs), d.row_stride * es);
+  return hipGetLastError();
+}
+
+template <typename T, bool WEIGHTED>
+static hipError_t combine_rows(const DispatchShape& d, const void* ys, const int32_t* s2r, const float* w, void* y,
+                               hipStream_t s) {
+  constexpr int cols = 256 * Elem<T>::kVec;
+  combine_rows_kernel<T, WEIGHTED><<<dim3((unsigned)((d.H + cols - 1) / cols), token_grid(d.T)), 256, 0, s>>>(
+      static_cast<const T*>(ys), d.row_stride, s2r, w, d.T, d.k, d.max_rows, d.H, static_cast<T*>(y), d.token_stride);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_rows(const DispatchShape& d, const void* ys, const int32_t* s2r, const float* w, void* y,
+                               hipStream_t s) {
+  if (d.dtype == 0) return w ? combine_rows<Bf16, true>(d, ys, s2r, w, y, s) : combine_rows<Bf16, false>(d, ys, s2r, w, y, s);
+  if (d.dtype == 1) return w ? combine_rows<F16, true>(d, ys, s2r, w, y, s) : combine_rows<F16, false>(d, ys, s2r, w, y, s);
+  return w ? combine_rows<float, true>(d, ys, s2r, w, y, s) : combine_rows<float, false>(d, ys, s2r, w, y, s);
+}
+
+template <typename T>
+static hipError_t combine_backward(const DispatchShape& d, const void* dy, const void* ys, const int32_t* s2r,
+                                   const float* w, void* dys, float* dw, const int32_t* ids, float* dlogits,
+                                   hipStream_t s) {
+  combine_backward_kernel<T, 8><<<token_grid(d.T), 512, 0, s>>>(
+      static_cast<const T*>(dy), d.token_stride, static_cast<const T*>(ys), d.row_stride, s2r, w, d.T, d.k, d.max_rows,
+      d.H, static_cast<T*>(dys), dw, ids, d.E, dlogits);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_backward(const DispatchShape& d, const void* dy, const void* ys, const int32_t* s2r,
+                                   const float* w, void* dys, float* dw, const int32_t* ids, float* dlogits,
+                                   hipStream_t s) {
+  if (d.dtype == 0) return combine_backward<Bf16>(d, dy, ys, s2r, w, dys, dw, ids, dlogits, s);
+  if (d.dtype == 1) return combine_backward<F16>(d, dy, ys, s2r, w, dys, dw, ids, dlogits, s);
+  return combine_backward<float>(d, dy, ys, s2r, w, dys, dw, ids, dlogits, s);
+}
+
+}  // namespace moe

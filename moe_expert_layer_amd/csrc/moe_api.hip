@@ -478,4 +478,150 @@ moe_status moe_unpack_scales(int32_t rows, int32_t groups, const int32_t* packed
   return ok();
 }
 
+// ---------------------------------------------------------------------------------------
+// tokens in expert order and back
+
+namespace {
+
+constexpr int kMaxDispatchHidden = 1 << 20;
+constexpr long long kMaxStride = 1LL << 40;
+
+moe_status check_dispatch_desc(const moe_dispatch_desc* d) {
+  if (!d) return fail(MOE_ERR_NULL, "desc is NULL");
+  if (d->num_tokens < 0) return fail(MOE_ERR_INVALID_DESC, "num_tokens %d < 0", d->num_tokens);
+  if (d->hidden < 1 || d->hidden > kMaxDispatchHidden)
+    return fail(MOE_ERR_INVALID_DESC, "hidden %d outside [1, %d]", d->hidden, kMaxDispatchHidden);
+  if (d->num_experts < 1 || d->num_experts > moe::kMaxExperts)
+    return fail(MOE_ERR_INVALID_DESC, "num_experts %d outside [1, %d]", d->num_experts, moe::kMaxExperts);
+  if (d->num_local < 1 || d->local_begin < 0 || (long long)d->local_begin + d->num_local > d->num_experts)
+    return fail(MOE_ERR_INVALID_DESC, "local range [%d, %d + %d) not inside [0, %d)", d->local_begin, d->local_begin,
+                d->num_local, d->num_experts);
+  if (d->topk < 1 || d->topk > moe::kMaxTopk)
+    return fail(MOE_ERR_INVALID_DESC, "topk %d outside [1, %d]", d->topk, moe::kMaxTopk);
+  const long long slots = (long long)d->num_tokens * d->topk;
+  if (slots >= (1LL << 31)) return fail(MOE_ERR_INVALID_DESC, "num_tokens * topk must be < 2^31");
+  if (d->dtype < MOE_DT_BF16 || d->dtype > MOE_DT_U8) return fail(MOE_ERR_INVALID_DESC, "dtype %d unknown", d->dtype);
+  if (d->max_rows < 0 || d->max_rows > slots)
+    return fail(MOE_ERR_INVALID_DESC, "max_rows %d outside [0, num_tokens * topk]", d->max_rows);
+  for (const long long stride : {(long long)d->token_stride, (long long)d->row_stride})
+    if (stride != 0 && (stride < d->hidden || stride > kMaxStride))
+      return fail(MOE_ERR_INVALID_DESC, "stride %lld neither 0 nor in [hidden, 2^40]", stride);
+  return MOE_OK;
+}
+
+// the descriptor of a call that adds up values
+moe_status check_dispatch_float(const moe_dispatch_desc* d) {
+  if (moe_status st = check_dispatch_desc(d)) return st;
+  if (d->dtype == MOE_DT_U8) return fail(MOE_ERR_UNSUPPORTED, "bytes can be dispatched, not summed");
+  return MOE_OK;
+}
+
+moe::DispatchShape dispatch_shape(const moe_dispatch_desc& d) {
+  moe::DispatchShape s;
+  s.T = d.num_tokens; s.H = d.hidden; s.E = d.num_experts; s.k = d.topk; s.dtype = d.dtype;
+  s.max_rows = d.max_rows ? d.max_rows : d.num_tokens * d.topk;
+  s.token_stride = d.token_stride ? d.token_stride : d.hidden;
+  s.row_stride = d.row_stride ? d.row_stride : d.hidden;
+  return s;
+}
+
+struct SortLayout {
+  size_t chunk_cnt, chunk_base, plan, total;
+};
+
+SortLayout sort_layout(const moe_dispatch_desc& d) {
+  const size_t NB = (size_t)d.num_local + 1;
+  const size_t nchunks = ((size_t)d.num_tokens * d.topk + moe::kPermChunk - 1) / moe::kPermChunk;
+  SortLayout L{};
+  L.chunk_cnt = 0;
+  L.chunk_base = align_up(nchunks * NB * 4);
+  L.plan = 2 * L.chunk_base;
+  L.total = L.plan + align_up(NB * 4);
+  return L;
+}
+
+}  // namespace
+
+moe_status moe_sort_workspace_size(const moe_dispatch_desc* d, size_t* bytes) {
+  if (moe_status st = check_dispatch_desc(d)) return st;
+  if (!bytes) return fail(MOE_ERR_NULL, "bytes is NULL");
+  *bytes = sort_layout(*d).total;
+  return ok();
+}
+
+moe_status moe_sort_tokens(const moe_dispatch_desc* d, const int32_t* ids, int32_t* counts, int32_t* offsets,
+                           int32_t* r2s, int32_t* s2r, void* ws, size_t ws_bytes, void* stream) {
+  if (moe_status st = check_dispatch_desc(d)) return st;
+  if (d->num_tokens == 0) return ok();
+  if (!ids || !counts || !offsets || !r2s || !s2r)
+    return fail(MOE_ERR_NULL, "topk_ids/counts/offsets/row_to_slot/slot_to_row NULL");
+  if (misaligned(ids, 4) || misaligned(counts, 4) || misaligned(offsets, 4) || misaligned(r2s, 4) || misaligned(s2r, 4))
+    return fail(MOE_ERR_MISALIGNED, "an int32 array is not 4-byte aligned");
+  const SortLayout L = sort_layout(*d);
+  if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+  if (misaligned(ws, kAlign)) return fail(MOE_ERR_MISALIGNED, "workspace not 256-byte aligned");
+  if (ws_bytes < L.total) return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes < required %zu", ws_bytes, L.total);
+  if (moe_status st = check_device()) return st;
+  // the permute also writes a GEMM tile plan (here for 128-row tiles), which stays in the workspace
+  MOE_TRY_HIP(moe::launch_permute(ids, d->num_tokens * d->topk, d->local_begin, d->num_local,
+                                  region<int32_t>(ws, L.chunk_cnt), region<int32_t>(ws, L.chunk_base), counts, offsets,
+                                  r2s, s2r, 128, region<int32_t>(ws, L.plan), (hipStream_t)stream));
+  return ok();
+}
+
+moe_status moe_dispatch(const moe_dispatch_desc* d, const void* x, const int32_t* s2r, void* xs, void* stream) {
+  if (moe_status st = check_dispatch_desc(d)) return st;
+  if (d->num_tokens == 0) return ok();
+  if (!x || !s2r || !xs) return fail(MOE_ERR_NULL, "x/slot_to_row/xs NULL");
+  const size_t es = (size_t)moe::dtype_bytes(d->dtype);
+  if (misaligned(x, es) || misaligned(xs, es) || misaligned(s2r, 4))
+    return fail(MOE_ERR_MISALIGNED, "x/xs/slot_to_row not aligned to its elements");
+  if (moe_status st = check_device()) return st;
+  MOE_TRY_HIP(moe::launch_dispatch(dispatch_shape(*d), x, s2r, xs, (hipStream_t)stream));
+  return ok();
+}
+
+moe_status moe_dispatch_backward(const moe_dispatch_desc* d, const void* dxs, const int32_t* s2r, void* dx,
+                                 void* stream) {
+  if (moe_status st = check_dispatch_float(d)) return st;
+  if (d->num_tokens == 0) return ok();
+  if (!dxs || !s2r || !dx) return fail(MOE_ERR_NULL, "dxs/slot_to_row/dx NULL");
+  const size_t es = (size_t)moe::dtype_bytes(d->dtype);
+  if (misaligned(dxs, es) || misaligned(dx, es) || misaligned(s2r, 4))
+    return fail(MOE_ERR_MISALIGNED, "dxs/dx/slot_to_row not aligned to its elements");
+  if (moe_status st = check_device()) return st;
+  MOE_TRY_HIP(moe::launch_combine_rows(dispatch_shape(*d), dxs, s2r, nullptr, dx, (hipStream_t)stream));
+  return ok();
+}
+
+moe_status moe_combine(const moe_dispatch_desc* d, const void* ys, const int32_t* s2r, const float* w, void* y,
+                       void* stream) {
+  if (moe_status st = check_dispatch_float(d)) return st;
+  if (d->num_tokens == 0) return ok();
+  if (!ys || !s2r || !w || !y) return fail(MOE_ERR_NULL, "ys/slot_to_row/topk_w/y NULL");
+  const size_t es = (size_t)moe::dtype_bytes(d->dtype);
+  if (misaligned(ys, es) || misaligned(y, es) || misaligned(s2r, 4) || misaligned(w, 4))
+    return fail(MOE_ERR_MISALIGNED, "ys/y/slot_to_row/topk_w not aligned to its elements");
+  if (moe_status st = check_device()) return st;
+  MOE_TRY_HIP(moe::launch_combine_rows(dispatch_shape(*d), ys, s2r, w, y, (hipStream_t)stream));
+  return ok();
+}
+
+moe_status moe_combine_backward(const moe_dispatch_desc* d, const void* dy, const void* ys, const int32_t* s2r,
+                                const float* w, void* dys, float* dw, const int32_t* ids, float* opt_dlogits,
+                                void* stream) {
+  if (moe_status st = check_dispatch_float(d)) return st;
+  if (d->num_tokens == 0) return ok();
+  if (!dy || !ys || !s2r || !w || !dys || !dw) return fail(MOE_ERR_NULL, "dy/ys/slot_to_row/topk_w/dys/dw NULL");
+  if (opt_dlogits && !ids) return fail(MOE_ERR_NULL, "dlogits wanted without topk_ids");
+  const size_t es = (size_t)moe::dtype_bytes(d->dtype);
+  if (misaligned(dy, es) || misaligned(ys, es) || misaligned(dys, es) || misaligned(s2r, 4) || misaligned(w, 4) ||
+      misaligned(dw, 4) || misaligned(ids, 4) || misaligned(opt_dlogits, 4))
+    return fail(MOE_ERR_MISALIGNED, "a tensor is not aligned to its elements");
+  if (moe_status st = check_device()) return st;
+  MOE_TRY_HIP(moe::launch_combine_backward(dispatch_shape(*d), dy, ys, s2r, w, dys, dw, ids, opt_dlogits,
+                                           (hipStream_t)stream));
+  return ok();
+}
+
 }  // extern "C"

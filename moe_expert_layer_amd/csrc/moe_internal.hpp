@@ -63,4 +63,20 @@ hipError_t launch_unpack_scales(const int32_t* packed, int M, int G, uint8_t* sf
 hipError_t launch_combine(const float* y2, const int32_t* slot_to_row, const float* topk_w, int T, int H, int k,
                           const int32_t* r_total, int S, uint16_t* y, hipStream_t s);
 
+// tokens in expert order and back ----------------------------------------------
+// dtype: moe_dtype (0 bf16, 1 f16, 2 f32, 3 bytes); strides in elements; a map entry outside
+// [0, max_rows) means the slot has no row
+struct DispatchShape {
+  int T, H, E, k, dtype, max_rows;
+  long long token_stride, row_stride;
+};
+constexpr long long dtype_bytes(int dtype) { return dtype == 2 ? 4 : dtype == 3 ? 1 : 2; }
+hipError_t launch_dispatch(const DispatchShape& d, const void* x, const int32_t* slot_to_row, void* xs, hipStream_t s);
+// w null: the plain sum of the token's rows (the gradient of launch_dispatch)
+hipError_t launch_combine_rows(const DispatchShape& d, const void* ys, const int32_t* slot_to_row, const float* w,
+                               void* y, hipStream_t s);
+hipError_t launch_combine_backward(const DispatchShape& d, const void* dy, const void* ys, const int32_t* slot_to_row,
+                                   const float* w, void* dys, float* dw, const int32_t* ids, float* dlogits,
+                                   hipStream_t s);
+
 }  // namespace moe
