@@ -379,6 +379,65 @@ moe_status moe_combine_backward(const moe_dispatch_desc* desc, const void* dy, c
                                 const int32_t* slot_to_row, const float* topk_w, void* dys, float* dw,
                                 const int32_t* topk_ids, float* opt_dlogits, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (MXFP4): quantisation, the values back, and the product.
+ *
+ * A row of K values is K/2 bytes of E2M1 codes (element 2i in the low nibble of byte i) and one
+ * UE8M0 scale byte per 32 values: the format of the layer's MXFP4 weights.  The scale bytes of M
+ * rows lie row-major [M, K/32] (MOE_SF_ROW_MAJOR: what moe_layer reads as w1_sf and w2_sf) or
+ * packed (MOE_SF_PACKED_MN: int32 words as moe_pack_scales writes them, here of 4 blocks of 32:
+ * word (m, j) at index j * aligned_M + m, aligned_M = M rounded up to 4, ceil(K/128) * aligned_M
+ * words, padding zero).  Weights [E, N, K] are E*N rows. */
+
+typedef struct {
+  int32_t rows;          /* M, 0 to 2^30 */
+  int32_t k;             /* K, a positive multiple of 32, at most 2^20 */
+  int32_t dtype;         /* moe_dtype of the values: bf16, f16 or f32 */
+  int32_t scale_layout;  /* moe_sf_layout of sf */
+  int64_t stride;        /* elements between rows of the values; 0 = K */
+} moe_mxfp4_desc;
+
+/* values [M, K] -> codes [M, K/2] and sf.  Per block of 32 the scale is 2^e with the smallest e
+ * such that 6 * 2^e >= amax (byte e + 127 clamped to [0, 254]; 127 for an all-zero block), codes
+ * E2M1 round-to-nearest-even of v * 2^-e: no value saturates.  A block with a NaN or an infinity
+ * gets byte 255 (UE8M0's NaN) and codes 0: the product's rows or columns that read it, and its
+ * dequantised values, are NaN (moe_layer takes no such weights).  Deterministic and exact.
+ * codes 16-byte aligned, packed sf 4-byte, values aligned to their element; no workspace.
+ * Stream, validation and error rules are those at the top of this file; rows = 0 launches
+ * nothing. */
+moe_status moe_quantize_mxfp4(const moe_mxfp4_desc* desc, const void* values, uint8_t* codes, void* sf, void* stream);
+
+/* The inverse: values = E2M1 code * 2^(byte - 127), rounded to nearest even to desc->dtype (exact
+ * for f32; bf16 and f16 overflow to infinity where the value does).  Byte 255 gives NaN.  The
+ * padding of packed scales is not read. */
+moe_status moe_dequantize_mxfp4(const moe_mxfp4_desc* desc, const uint8_t* codes, const void* sf, void* values,
+                                void* stream);
+
+typedef struct {
+  int32_t rows;            /* rows of A and C, 0 to 2^30 */
+  int32_t n;               /* N, columns of C = rows of B per group, 1 to 2^24 */
+  int32_t k;               /* K, a positive multiple of 32, at most 2^20 */
+  int32_t groups;          /* 1 to 1024 */
+  int32_t out_dtype;       /* moe_dtype of C: bf16, f16 or f32 */
+  int32_t a_scale_layout;  /* moe_sf_layout; row-major needs K a multiple of 128 */
+  int32_t b_scale_layout;
+  int32_t variant;         /* tiles: -1 = by size */
+  int64_t out_stride;      /* elements between rows of C; 0 = N */
+} moe_mxfp4_gemm_desc;
+
+/* Grouped product of MXFP4 rows with MXFP4 weights, float32 sums, one rounding to the type of C:
+ *   c[r, n] = sum_k a[r, k] * b[e, n, k]   for offsets[e] <= r < offsets[e + 1]
+ * a [rows, K] (say, quantised tokens in expert order), b [groups, N, K], offsets int32
+ * [groups + 1] on the device, ascending from 0 (moe_sort_tokens), or NULL with one group: all rows
+ * (a plain product).  Rows at or past offsets[groups] are neither read nor written; offsets outside
+ * [0, rows] or descending are cut to it.  The sum's order depends on the sizes only, so results
+ * are the same from run to run.  a, b and row-major scales 16-byte aligned, packed scales 4-byte,
+ * c aligned to its element; c must not overlap the inputs.  No workspace.  Scale byte 255 makes
+ * every result that reads it NaN.  Errors as for the other calls; MOE_ERR_UNSUPPORTED for
+ * row-major scales with K not a multiple of 128 (moe_pack_scales packs them). */
+moe_status moe_mxfp4_gemm(const moe_mxfp4_gemm_desc* desc, const uint8_t* a, const void* a_sf, const uint8_t* b,
+                          const void* b_sf, const int32_t* offsets, void* c, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -51,6 +51,17 @@ class MoeDispatchDesc(ctypes.Structure):
     ]
 
 
+class MoeMxfp4Desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("k", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale_layout", ctypes.c_int32), ("stride", ctypes.c_int64)]
+
+
+class MoeMxfp4GemmDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("a_scale_layout", ctypes.c_int32), ("b_scale_layout", ctypes.c_int32),
+                ("variant", ctypes.c_int32), ("out_stride", ctypes.c_int64)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{status_str(status)}: {msg}")
@@ -103,6 +114,9 @@ def lib():
             "moe_dispatch_backward": [DD, P, P, P, VP],
             "moe_combine": [DD, P, P, P, P, VP],
             "moe_combine_backward": [DD, P, P, P, P, P, P, P, P, VP],
+            "moe_quantize_mxfp4": [ctypes.POINTER(MoeMxfp4Desc), P, P, P, VP],
+            "moe_dequantize_mxfp4": [ctypes.POINTER(MoeMxfp4Desc), P, P, P, VP],
+            "moe_mxfp4_gemm": [ctypes.POINTER(MoeMxfp4GemmDesc), P, P, P, P, P, P, VP],
         }.items():
             f = getattr(L, name)
             f.restype, f.argtypes = I32, args
@@ -394,3 +408,60 @@ def moe_combine_backward(desc, dy, ys, slot_to_row, topk_w, dys, dw, topk_ids=No
         _array("dlogits", dlogits, torch.float32, desc.num_tokens * desc.num_experts, dev)
     _launch(lib().moe_combine_backward, dev, stream, ctypes.byref(desc), dy.data_ptr(), ys.data_ptr(),
             slot_to_row.data_ptr(), topk_w.data_ptr(), dys.data_ptr(), dw.data_ptr(), _ptr(topk_ids), _ptr(dlogits))
+
+
+def make_mxfp4_desc(rows: int, k: int, dtype: str = "bf16", scale_layout: str = "rows", stride: int = 0) -> MoeMxfp4Desc:
+    """Descriptor of MXFP4 rows and the values they come from.  dtype: "bf16", "f16" or "f32"; scale_layout: "rows"
+    (UE8M0 bytes [rows, k / 32], what moe_layer's MXFP4 weights have) or "packed" (int32 words
+    [ceil(k / 128), rows rounded up to 4]); stride: elements between rows of the values (0 = k)."""
+    return MoeMxfp4Desc(rows, k, DTYPES[dtype], SCALE_LAYOUTS[scale_layout], stride)
+
+
+def make_mxfp4_gemm_desc(rows: int, n: int, k: int, groups: int = 1, out_dtype: str = "bf16",
+                         a_scale_layout: str = "packed", b_scale_layout: str = "packed", variant: int = -1,
+                         out_stride: int = 0) -> MoeMxfp4GemmDesc:
+    """Descriptor of a grouped MXFP4 product [rows, k] x [groups, n, k] -> [rows, n]."""
+    return MoeMxfp4GemmDesc(rows, n, k, groups, DTYPES[out_dtype], SCALE_LAYOUTS[a_scale_layout],
+                            SCALE_LAYOUTS[b_scale_layout], variant, out_stride)
+
+
+def _codes_and_scales(name, codes, sf, rows, k, layout, dev):
+    import torch
+    _array(name, codes, torch.uint8, rows * (k // 2), dev)
+    if layout == MOE_SF_PACKED_MN:
+        _array(name + "_sf", sf, torch.int32, (k // 32 + 3) // 4 * ((rows + 3) // 4 * 4), dev)
+    else:
+        _array(name + "_sf", sf, torch.uint8, rows * (k // 32), dev)
+
+
+def moe_quantize_mxfp4(desc, values, codes, sf, stream=None):
+    """values [rows, k] -> E2M1 codes uint8 [rows, k / 2] and UE8M0 scales (uint8, or int32 words when packed)."""
+    dev = _device_of(values)
+    _rows_tensor("values", values, _torch_dtype(desc.dtype), desc.rows, desc.k, desc.stride or desc.k, dev)
+    _codes_and_scales("codes", codes, sf, desc.rows, desc.k, desc.scale_layout, dev)
+    _launch(lib().moe_quantize_mxfp4, dev, stream, ctypes.byref(desc), values.data_ptr(), codes.data_ptr(), sf.data_ptr())
+
+
+def moe_dequantize_mxfp4(desc, codes, sf, values, dtype: Optional[str] = None, stream=None):
+    """The values [rows, k] of codes and scales, in the descriptor's dtype (or the one named)."""
+    if dtype is not None and DTYPES[dtype] != desc.dtype:
+        desc = MoeMxfp4Desc(desc.rows, desc.k, DTYPES[dtype], desc.scale_layout, desc.stride)
+    dev = _device_of(codes)
+    _codes_and_scales("codes", codes, sf, desc.rows, desc.k, desc.scale_layout, dev)
+    _rows_tensor("values", values, _torch_dtype(desc.dtype), desc.rows, desc.k, desc.stride or desc.k, dev)
+    _launch(lib().moe_dequantize_mxfp4, dev, stream, ctypes.byref(desc), codes.data_ptr(), sf.data_ptr(),
+            values.data_ptr())
+
+
+def moe_mxfp4_gemm(desc, a, a_sf, b, b_sf, offsets, c, stream=None):
+    """c[r] = a[r] @ b[e].T for the rows of each group e (offsets int32 [groups + 1]; None: one group of all rows);
+    a, b: E2M1 codes with their scales, c [rows, n].  Rows past the last group are left as they were."""
+    import torch
+    dev = _device_of(a)
+    _codes_and_scales("a", a, a_sf, desc.rows, desc.k, desc.a_scale_layout, dev)
+    _codes_and_scales("b", b, b_sf, desc.groups * desc.n, desc.k, desc.b_scale_layout, dev)
+    if offsets is not None:
+        _array("offsets", offsets, torch.int32, desc.groups + 1, dev)
+    _rows_tensor("c", c, _torch_dtype(desc.out_dtype), desc.rows, desc.n, desc.out_stride or desc.n, dev)
+    _launch(lib().moe_mxfp4_gemm, dev, stream, ctypes.byref(desc), a.data_ptr(), a_sf.data_ptr(), b.data_ptr(),
+            b_sf.data_ptr(), _ptr(offsets), c.data_ptr())

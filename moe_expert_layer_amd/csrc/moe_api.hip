@@ -624,4 +624,116 @@ moe_status moe_combine_backward(const moe_dispatch_desc* d, const void* dy, cons
   return ok();
 }
 
+// ---------------------------------------------------------------------------------------
+// microscaled 4-bit floating point
+
+namespace {
+
+constexpr int kMaxMxRows = 1 << 30;
+constexpr int kMaxMxK = 1 << 20;
+constexpr int kMaxMxN = 1 << 24;
+constexpr int kMaxMxGroups = 1024;
+
+moe_status check_mx_k(int32_t k) {
+  if (k < 32 || k % 32 || k > kMaxMxK)
+    return fail(MOE_ERR_INVALID_DESC, "k %d not a positive multiple of 32 up to %d", k, kMaxMxK);
+  return MOE_OK;
+}
+
+moe_status check_mx_layout(int32_t layout) {
+  if (layout != MOE_SF_ROW_MAJOR && layout != MOE_SF_PACKED_MN)
+    return fail(MOE_ERR_INVALID_DESC, "scale_layout %d unknown", layout);
+  return MOE_OK;
+}
+
+moe_status check_mx_float(int32_t dtype) {
+  if (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16 && dtype != MOE_DT_F32)
+    return fail(MOE_ERR_INVALID_DESC, "dtype %d is not bf16, f16 or f32", dtype);
+  return MOE_OK;
+}
+
+moe_status check_mx_call(const moe_mxfp4_desc* d, const void* values, const void* codes, const void* sf) {
+  if (!d) return fail(MOE_ERR_NULL, "desc is NULL");
+  if (d->rows < 0 || d->rows > kMaxMxRows)
+    return fail(MOE_ERR_INVALID_DESC, "rows %d outside [0, %d]", d->rows, kMaxMxRows);
+  if (moe_status st = check_mx_k(d->k)) return st;
+  if (moe_status st = check_mx_float(d->dtype)) return st;
+  if (moe_status st = check_mx_layout(d->scale_layout)) return st;
+  if (d->stride != 0 && (d->stride < d->k || d->stride > kMaxStride))
+    return fail(MOE_ERR_INVALID_DESC, "stride %lld neither 0 nor in [k, 2^40]", (long long)d->stride);
+  if (d->rows == 0) return MOE_OK;
+  if (!values || !codes || !sf) return fail(MOE_ERR_NULL, "values/codes/sf NULL");
+  if (misaligned(values, (size_t)moe::dtype_bytes(d->dtype)) || misaligned(codes, 16) ||
+      (d->scale_layout == MOE_SF_PACKED_MN && misaligned(sf, 4)))
+    return fail(MOE_ERR_MISALIGNED, "values / codes / sf misaligned");
+  return MOE_OK;
+}
+
+int packed_rows(int32_t layout, long long rows) { return layout == MOE_SF_PACKED_MN ? (int)((rows + 3) / 4 * 4) : 0; }
+
+}  // namespace
+
+moe_status moe_quantize_mxfp4(const moe_mxfp4_desc* d, const void* values, uint8_t* codes, void* sf, void* stream) {
+  if (moe_status st = check_mx_call(d, values, codes, sf)) return st;
+  if (d->rows == 0) return ok();
+  if (moe_status st = check_device()) return st;
+  MOE_TRY_HIP(moe::launch_quantize_mxfp4(values, d->dtype, d->stride ? d->stride : d->k, d->rows, d->k, codes,
+                                         static_cast<uint8_t*>(sf), packed_rows(d->scale_layout, d->rows),
+                                         (hipStream_t)stream));
+  return ok();
+}
+
+moe_status moe_dequantize_mxfp4(const moe_mxfp4_desc* d, const uint8_t* codes, const void* sf, void* values,
+                                void* stream) {
+  if (moe_status st = check_mx_call(d, values, codes, sf)) return st;
+  if (d->rows == 0) return ok();
+  if (moe_status st = check_device()) return st;
+  MOE_TRY_HIP(moe::launch_dequantize_mxfp4(codes, static_cast<const uint8_t*>(sf), packed_rows(d->scale_layout, d->rows),
+                                           d->rows, d->k, values, d->dtype, d->stride ? d->stride : d->k,
+                                           (hipStream_t)stream));
+  return ok();
+}
+
+moe_status moe_mxfp4_gemm(const moe_mxfp4_gemm_desc* d, const uint8_t* a, const void* a_sf, const uint8_t* b,
+                          const void* b_sf, const int32_t* offsets, void* c, void* stream) {
+  if (!d) return fail(MOE_ERR_NULL, "desc is NULL");
+  if (d->rows < 0 || d->rows > kMaxMxRows)
+    return fail(MOE_ERR_INVALID_DESC, "rows %d outside [0, %d]", d->rows, kMaxMxRows);
+  if (d->n < 1 || d->n > kMaxMxN) return fail(MOE_ERR_INVALID_DESC, "n %d outside [1, %d]", d->n, kMaxMxN);
+  if (d->groups < 1 || d->groups > kMaxMxGroups)
+    return fail(MOE_ERR_INVALID_DESC, "groups %d outside [1, %d]", d->groups, kMaxMxGroups);
+  if ((long long)d->groups * d->n > kMaxMxRows)
+    return fail(MOE_ERR_INVALID_DESC, "groups * n above %d", kMaxMxRows);
+  if (moe_status st = check_mx_k(d->k)) return st;
+  if (moe_status st = check_mx_float(d->out_dtype)) return st;
+  if (moe_status st = check_mx_layout(d->a_scale_layout)) return st;
+  if (moe_status st = check_mx_layout(d->b_scale_layout)) return st;
+  if (d->variant != -1) return fail(MOE_ERR_INVALID_DESC, "variant %d unknown", d->variant);
+  if (d->out_stride != 0 && (d->out_stride < d->n || d->out_stride > kMaxStride))
+    return fail(MOE_ERR_INVALID_DESC, "out_stride %lld neither 0 nor in [n, 2^40]", (long long)d->out_stride);
+  if (d->k % 128 && (d->a_scale_layout == MOE_SF_ROW_MAJOR || d->b_scale_layout == MOE_SF_ROW_MAJOR))
+    return fail(MOE_ERR_UNSUPPORTED, "row-major scales need k %% 128 = 0 (k = %d): pack them", d->k);
+  if (d->rows == 0) return ok();
+  if (!a || !a_sf || !b || !b_sf || !c) return fail(MOE_ERR_NULL, "a/a_sf/b/b_sf/c NULL");
+  if (!offsets && d->groups != 1) return fail(MOE_ERR_NULL, "offsets NULL with %d groups", d->groups);
+  if (misaligned(a, 16) || misaligned(b, 16) || misaligned(a_sf, d->a_scale_layout == MOE_SF_PACKED_MN ? 4 : 16) ||
+      misaligned(b_sf, d->b_scale_layout == MOE_SF_PACKED_MN ? 4 : 16) || misaligned(offsets, 4) ||
+      misaligned(c, (size_t)moe::dtype_bytes(d->out_dtype)))
+    return fail(MOE_ERR_MISALIGNED, "a / a_sf / b / b_sf / offsets / c misaligned");
+  if (moe_status st = check_device()) return st;
+  moe::Mxfp4GemmArgs g{};
+  g.A = a; g.A_sf = static_cast<const uint8_t*>(a_sf); g.B = b; g.B_sf = static_cast<const uint8_t*>(b_sf);
+  g.offsets = offsets; g.C = c;
+  g.rows = d->rows; g.N = d->n; g.K = d->k; g.groups = d->groups;
+  g.c_stride = d->out_stride ? d->out_stride : d->n;
+  auto scale_strides = [&](int32_t layout, long long rows, long long& row_mul, long long& word_mul) {
+    row_mul = layout == MOE_SF_PACKED_MN ? 4 : d->k / 32;
+    word_mul = layout == MOE_SF_PACKED_MN ? 4LL * packed_rows(layout, rows) : 4;
+  };
+  scale_strides(d->a_scale_layout, d->rows, g.a_row_mul, g.a_word_mul);
+  scale_strides(d->b_scale_layout, (long long)d->groups * d->n, g.b_row_mul, g.b_word_mul);
+  MOE_TRY_HIP(moe::launch_mxfp4_gemm(g, d->out_dtype, d->variant, (hipStream_t)stream));
+  return ok();
+}
+
 }  // extern "C"
