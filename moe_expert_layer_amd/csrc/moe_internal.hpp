@@ -27,6 +27,9 @@ struct Shape {
   float clamp, alpha, bias;
 };
 
+// compute units of the current device (cached per device)
+int device_cus();
+
 // route + permute ----------------------------------------------------------
 hipError_t launch_route_topk(const float* logits, int T, int E, int k, int32_t* ids, float* w, hipStream_t s);
 // buckets: EL local experts + 1 trailing bucket for non-local slots.  Also writes the GEMM
