@@ -29,6 +29,30 @@ __device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t ld
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds)
                : "memory", "m0");
 }
+// the same from a buffer: its base and length sit in a four-dword descriptor in SGPRs, soff is a
+// uniform byte offset, and a lane whose voff + soff reaches past the length reads nothing there (the
+// hardware checks every load: voff >= length - soff is out of range, so soff is kept within the
+// length).  The length is cut to 2^31 - 1, past which no caller's offsets reach; a voff of kNowhere is
+// then out of range in every buffer.
+constexpr uint32_t kNowhere = 0x80000000u;
+typedef int v4i_srd __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ v4i_srd buffer_srd(const void* base, long long bytes) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint32_t len = bytes < 0x7fffffffLL ? (uint32_t)bytes : 0x7fffffffu;
+  return v4i_srd{(int)__builtin_amdgcn_readfirstlane((uint32_t)b),
+                 (int)(__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) & 0xffffu),
+                 (int)__builtin_amdgcn_readfirstlane(len), 0x00020000};  // raw buffer, 32-bit format
+}
+__device__ __forceinline__ void dma16_buffer(v4i_srd srd, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(srd),
+               "s"(soff), "s"(lds)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void dma4_buffer(v4i_srd srd, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(voff), "s"(srd),
+               "s"(soff), "s"(lds)
+               : "memory", "m0");
+}
 template <int N>
 __device__ __forceinline__ void wait_vm_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");

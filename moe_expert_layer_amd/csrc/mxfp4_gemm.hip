@@ -134,38 +134,48 @@ __global__ __launch_bounds__(NW * 64) void mxfp4_gemm_rows_kernel(Mxfp4GemmArgs 
 // Tiles of BM rows x BN columns for groups with many rows.
 //
 // K advances 256 values a stage: 128 bytes (a cache line) of codes per operand row, brought from
-// global memory straight into one of two LDS slots, with the stage's two scale words per row.  The
-// NW waves each own a WTM x WTN part as 32 x 32 accumulators.  A lane of the 32x32x64 instruction
+// global memory straight into one of two LDS slots, and two scale words per row, into one of four.
+// The NW waves each own a WTM x WTN part as 32 x 32 accumulators.  A lane of the 32x32x64 instruction
 // holds one block of 32 of row lane % 32; half kb = lane / 32 of the lanes works through the four
 // blocks of the stage's scale word kb in four steps, so it reads one scale word per row and stage.
 // The fragments of the next step are read from LDS while the matrix instructions of this one run;
-// the stage boundary (wait for the next stage's loads, barrier, next loads issued into the slot just
-// read) sits before the last step's instructions, when every wave holds its last fragments.
+// the stage boundary (wait for the next stage's codes, barrier, loads of the stage after it into the
+// slot just read) sits before the last step's instructions, when every wave holds its last fragments.
+//
+// Loads of a wave complete in order, so what is issued behind a stage's codes may stay in flight when
+// those are waited for: the scales of two stages further on, and one prefetch.  A prefetch is a 4-byte
+// load whose 64 lanes each touch the line of another row kAhead stages further on, shared out among
+// the workgroups of the XCD that read the same rows, so that the lines are on their way from HBM
+// before the stage's own loads ask the L2 for them.  Loads that have nothing to do (past the last
+// stage) are issued with a buffer of length 0: they read nothing and keep the counts alike.
 //
 // Weights are the instruction's first operand, so a lane's results are runs of four columns of one
-// row; a wave puts its part in type T into LDS (its own 32 KB of the slots) and stores whole 16-byte
-// chunks, 256 contiguous bytes a row.  Workgroups are persistent: each XCD has a contiguous range of
-// tiles, whose rows and columns of operands meet in its L2, and its workgroups take them in turn.
+// row; a wave puts them in type T into its part of the second slot, 32 rows x 256 bytes at a time, and
+// stores whole 16-byte chunks, while the next tile's first stage lands in the first slot.  Workgroups
+// are persistent: each XCD has a contiguous range of tiles, whose rows and columns of operands meet in
+// its L2, and its workgroups take them in turn.
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
+constexpr int kAhead = 1;       // stages between a line's prefetch and its load
 constexpr int kTileGroupN = 8;  // column tiles that go together in the tile order
 
 template <int BM, int BN, int NW, int WTM, int WTN>
 struct TileCfg {
   static constexpr int NT = NW * 64, WM = BM / WTM, MI = WTM / 32, NI = WTN / 32;
-  static constexpr int kRowB = 128;                       // bytes of codes per row and stage
-  static constexpr int kA = BM * kRowB, kB = BN * kRowB;  // offsets in a stage: A, B, A's words, B's words
-  static constexpr int kSA = kA + kB, kSB = kSA + BM * 8;
-  static constexpr int kStage = kSB + BN * 8;
-  static constexpr int kPlan = 2 * kStage;
-  static constexpr int kADma = BM / 8 / NW, kBDma = BN / 8 / NW;                // 1 KB loads per wave and stage
-  static constexpr int kSaDma = BM * 2 / 64 / NW, kSbDma = BN * 2 / 64 / NW;  // 256-byte scale loads
-  static constexpr int kOutB = NW * WTM * 256;                                   // results staged in LDS
+  static constexpr int kRowB = 128;                  // bytes of codes per row and stage
+  static constexpr int kSlot = (BM + BN) * kRowB;    // A's rows, then B's
+  static constexpr int kScales = 2 * kSlot;          // four slots of [word][A's rows], [word][B's rows]
+  static constexpr int kScaleSlot = (BM + BN) * 8;
+  static constexpr int kJunk = kScales + 4 * kScaleSlot, kPlan = kJunk + 256;
+  static constexpr int kADma = BM / 8 / NW, kBDma = BN / 8 / NW;  // 1 KB loads per wave and stage
+  static constexpr int kSDma = (BM + BN) * 2 / 64 / NW;           // 256-byte loads of scale words
+  static constexpr int kTouch = (BM + BN) / 64 / NW;              // prefetches per wave and stage
+  static constexpr int kPer = kADma + kBDma + kSDma + kTouch;     // loads per wave and stage
   static_assert(WM * (BN / WTN) == NW && kADma * NW * 8 == BM && kBDma * NW * 8 == BN, "");
-  static_assert(kSaDma * NW * 32 == BM && kSbDma * NW * 32 == BN, "");
-  static_assert(kOutB <= 2 * kStage, "");
+  static_assert(kSDma * NW * 32 == BM + BN && BM % 64 == 0 && BN % 64 == 0 && kTouch >= 1, "");
+  static_assert(NW * 32 * 256 <= kSlot && WTN == 128, "the results' staging fits a slot, in passes of 256 bytes");
 };
 
 template <typename T, int BM, int BN, int NW, int WTM, int WTN>
@@ -203,170 +213,203 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
   // XCD x = blockIdx % 8 has tiles [x q + min(x, r), ...) of q = total / 8, r = total % 8
   const long long xq = total >> 3;
   const int x = blockIdx.x & 7, xr = (int)(total & 7);
-  const long long x_cnt = xq + (x < xr ? 1 : 0), x_base = x * xq + (x < xr ? x : xr);
+  const long long x_cnt = xq + (x < xr ? 1 : 0), x_base = x * xq + (x < xr ? x : xr), x_step = gridDim.x >> 3;
 
-  const int lrow = lane & 31, kb = lane >> 5;
-  const int wm = wave % C::WM, wn = wave / C::WM;
   const int ld = g.K / 2, nblk = g.K / 32, nwords = (nblk + 3) / 4, nst = (nwords + 1) / 2;
   const bool ktail = (nblk & 7) != 0;
   const uint32_t ring0 = lds_addr(lds);
-  // fragment addresses in a stage: chunk 4 kb + s of row r lies at (chunk ^ swz(r)); rows 32 apart
-  // differ in bit 2 of the swizzle
+
+  // a tile's operands: buffers that end with its rows and columns
+  struct Tile {
+    v4i_srd a, b;
+    const uint8_t* s;          // scale word 0 of the first row of the operand whose scales this wave loads
+    uint32_t s_len;
+    int row0, rows, n0, cols;
+    uint32_t pf[C::kTouch];    // the rows this lane prefetches, or kNowhere
+  };
+  auto locate = [&](long long p) {
+    const long long L = x_base + p;
+    int e = 0, hi = g.groups - 1;
+    const int mt = (int)(L / n_tiles);
+    while (e < hi) {  // the last group that starts at or before this row tile (it has rows)
+      const int mid = (e + hi + 1) >> 1;
+      if (s_plan[mid] <= mt) e = mid; else hi = mid - 1;
+    }
+    e = __builtin_amdgcn_readfirstlane(e);
+    const int first = __builtin_amdgcn_readfirstlane(s_plan[e]);
+    const int m_tiles = __builtin_amdgcn_readfirstlane(s_plan[e + 1]) - first;
+    const int li = (int)(L - (long long)first * n_tiles);
+    const int grp = li / (kTileGroupN * m_tiles);
+    const int gsz = min(n_tiles - grp * kTileGroupN, kTileGroupN);
+    const int idx = li - grp * kTileGroupN * m_tiles, m = idx / gsz, n = idx % gsz;
+    Tile t;
+    t.row0 = __builtin_amdgcn_readfirstlane(s_lo[e]) + m * BM;
+    t.rows = min(BM, __builtin_amdgcn_readfirstlane(s_hi[e]) - t.row0);
+    t.n0 = (grp * kTileGroupN + n) * BN;
+    t.cols = min(BN, g.N - t.n0);
+    const long long brow = (long long)e * g.N + t.n0;
+    t.a = buffer_srd(g.A + (long long)t.row0 * ld, (long long)t.rows * ld);
+    t.b = buffer_srd(g.B + brow * ld, (long long)t.cols * ld);
+    t.s = wave * C::kSDma < BM / 32 ? g.A_sf + t.row0 * g.a_row_mul : g.B_sf + brow * g.b_row_mul;
+    t.s_len = (uint32_t)(wave * C::kSDma < BM / 32 ? (t.rows - 1) * g.a_row_mul + 4 : (t.cols - 1) * g.b_row_mul + 4);
+    const int share = min(m_tiles, 4);
+#pragma unroll
+    for (int i = 0; i < C::kTouch; ++i) {
+      const int r = (wave * C::kTouch + i) * 64 + lane;  // rows of A, then of B
+      const bool mine = r < BM ? r < t.rows && r % gsz == n : r - BM < t.cols && (r - BM) % share == m % share;
+      t.pf[i] = mine ? (uint32_t)(r < BM ? r : r - BM) * (uint32_t)ld : kNowhere;
+    }
+    return t;
+  };
+
+  // load offsets of this lane: 16-byte chunk c of row r goes to chunk c ^ swz(r) of its LDS row
+  uint32_t a_off[C::kADma], b_off[C::kBDma], s_off[C::kSDma];
+#pragma unroll
+  for (int i = 0; i < C::kADma; ++i) {
+    const int r = (wave * C::kADma + i) * 8 + lane / 8;
+    a_off[i] = (uint32_t)r * (uint32_t)ld + (((lane & 7) ^ swz<8>(r)) << 4);
+  }
+#pragma unroll
+  for (int i = 0; i < C::kBDma; ++i) {
+    const int r = (wave * C::kBDma + i) * 8 + lane / 8;
+    b_off[i] = (uint32_t)r * (uint32_t)ld + (((lane & 7) ^ swz<8>(r)) << 4);
+  }
+  // the wave's scale loads are of one operand and one of its two words a stage
+  static_assert(BM / 64 % C::kSDma == 0 && BN / 64 % C::kSDma == 0, "");
+  const bool s_is_a = wave * C::kSDma < BM / 32;
+  const int s_q = s_is_a ? wave * C::kSDma : wave * C::kSDma - BM / 32;  // in loads of 64 rows of one word
+  const int s_word = s_is_a ? s_q / (BM / 64) : s_q / (BN / 64);
+  const long long s_word_mul = s_is_a ? g.a_word_mul : g.b_word_mul;
+#pragma unroll
+  for (int i = 0; i < C::kSDma; ++i)
+    s_off[i] = s_is_a ? (uint32_t)(((s_q + i) * 64 + lane) % BM) * (uint32_t)g.a_row_mul
+                      : (uint32_t)(((s_q + i) * 64 + lane) % BN) * (uint32_t)g.b_row_mul;
+
+  // load i of this wave for the stages that follow stage ks: codes of stage ks + 2 (past K they are the
+  // next row's, or lie past the buffer; they are cut below), scales of stage ks + 4, lines of stage
+  // ks + 2 + kAhead (of the last stage again where there is none)
+  auto issue = [&](const Tile& t, int i, int ks) {
+    if (i < C::kADma) {
+      dma16_buffer(t.a, a_off[i], (uint32_t)(ks + 2) * C::kRowB,
+                   ring0 + (uint32_t)(ks & 1) * C::kSlot + (wave * C::kADma + i) * 1024);
+    } else if (i < C::kADma + C::kBDma) {
+      const int k = i - C::kADma;
+      dma16_buffer(t.b, b_off[k], (uint32_t)(ks + 2) * C::kRowB,
+                   ring0 + (uint32_t)(ks & 1) * C::kSlot + BM * C::kRowB + (wave * C::kBDma + k) * 1024);
+    } else if (i < C::kADma + C::kBDma + C::kSDma) {
+      const int k = i - C::kADma - C::kBDma, q = wave * C::kSDma + k;
+      const int j = min(2 * (ks + 4) + s_word, nwords - 1);
+      dma4_buffer(buffer_srd(t.s + j * s_word_mul, t.s_len), s_off[k], 0u,
+                  ring0 + C::kScales + (uint32_t)(ks & 3) * C::kScaleSlot + q * 256);
+    } else {
+      const int k = i - C::kADma - C::kBDma - C::kSDma;
+      dma4_buffer((wave * C::kTouch + k) * 64 < BM ? t.a : t.b, t.pf[k], (uint32_t)min(ks + 2 + kAhead, nst - 1) * C::kRowB,
+                  ring0 + C::kJunk);
+    }
+  };
+
+  // fragment addresses in a slot: chunk 4 kb + s of row r; rows 32 apart differ in bit 2 of the swizzle
+  const int lrow = lane & 31, kb = lane >> 5;
+  const int wm = wave % C::WM, wn = wave / C::WM;
   const int ra = wm * WTM + lrow, rb = wn * WTN + lrow;
   const uint32_t fa = ra * C::kRowB + (((4 * kb) ^ swz<8>(ra)) << 4);
-  const uint32_t fb = C::kA + rb * C::kRowB + (((4 * kb) ^ swz<8>(rb)) << 4);
-  const uint32_t wa = C::kSA + (kb * BM + ra) * 4, wb = C::kSB + (kb * BN + rb) * 4;
+  const uint32_t fb = (BM + rb) * C::kRowB + (((4 * kb) ^ swz<8>(rb)) << 4);
+  const uint32_t wa = C::kScales + (kb * BM + ra) * 4, wb = C::kScales + (2 * BM + kb * BN + rb) * 4;
 
-  for (long long p = blockIdx.x >> 3; p < x_cnt; p += gridDim.x >> 3) {
-    const long long L = x_base + p;
-    int e = 0;
-    {
-      int hi = g.groups - 1;  // the last group that starts at or before this row tile (it has rows)
-      const int mt = (int)(L / n_tiles);
-      while (e < hi) {
-        const int mid = (e + hi + 1) >> 1;
-        if (s_plan[mid] <= mt) e = mid; else hi = mid - 1;
-      }
+  struct Frags {
+    v4i a[C::MI], b[C::NI];
+  };
+  struct Scales {
+    int a[C::MI], b[C::NI];
+  };
+  auto load = [&](int ks, int s, Frags& f) {
+    const uint8_t* st = lds + (ks & 1) * C::kSlot;
+#pragma unroll
+    for (int m = 0; m < C::MI; ++m)
+      f.a[m] = *reinterpret_cast<const v4i*>(st + (fa ^ (uint32_t)((s << 4) ^ ((m & 1) << 6))) + m * 32 * C::kRowB);
+#pragma unroll
+    for (int n = 0; n < C::NI; ++n)
+      f.b[n] = *reinterpret_cast<const v4i*>(st + (fb ^ (uint32_t)((s << 4) ^ ((n & 1) << 6))) + n * 32 * C::kRowB);
+  };
+  auto load_scales = [&](int ks, Scales& c) {
+    const uint8_t* st = lds + (ks & 3) * C::kScaleSlot;
+#pragma unroll
+    for (int m = 0; m < C::MI; ++m) c.a[m] = *reinterpret_cast<const int*>(st + wa + m * 128);
+#pragma unroll
+    for (int n = 0; n < C::NI; ++n) c.b[n] = *reinterpret_cast<const int*>(st + wb + n * 128);
+  };
+  // the last stage, where it lies past K for this lane: zero codes, and scales of 1 whatever the
+  // padding holds
+  auto cut = [&](int s, Frags& f) {
+    if (ktail && ((nst - 1) * 2 + kb) * 4 + s >= nblk) {
+#pragma unroll
+      for (int m = 0; m < C::MI; ++m) f.a[m] = v4i{0, 0, 0, 0};
     }
-    const int m_tiles = s_plan[e + 1] - s_plan[e];
-    const long long li = L - (long long)s_plan[e] * n_tiles;
-    const int grp = (int)(li / ((long long)kTileGroupN * m_tiles));
-    const int gsz = min(n_tiles - grp * kTileGroupN, kTileGroupN);
-    const int idx = (int)(li - (long long)grp * kTileGroupN * m_tiles);
-    const int row0 = s_lo[e] + idx / gsz * BM, rows = min(BM, s_hi[e] - row0);
-    const int n0 = (grp * kTileGroupN + idx % gsz) * BN, cols = min(BN, g.N - n0);
-
-    // sources; rows and columns past the end repeat the last one
-    const long long brow0 = (long long)e * g.N + n0;
-    const uint8_t* a_base = g.A + (long long)row0 * ld;
-    const uint8_t* b_base = g.B + brow0 * ld;
-    const uint8_t* sa_base = g.A_sf + row0 * g.a_row_mul;
-    const uint8_t* sb_base = g.B_sf + brow0 * g.b_row_mul;
-    uint32_t a_off[C::kADma], b_off[C::kBDma], a_c, sa_off[C::kSaDma], sb_off[C::kSbDma];
-    {
-      // load i of the wave covers rows 8 (wave * n + i) .. + 7: the swizzle of a row 8 further differs,
-      // so the chunk is computed per load and folded into the offset
+  };
+  auto cut_scales = [&](Scales& c) {
+    if (ktail) {
+      const int left = nblk - ((nst - 1) * 2 + kb) * 4;
+      const int keep = left >= 4 ? -1 : left <= 0 ? 0 : (1 << (8 * left)) - 1;
 #pragma unroll
-      for (int i = 0; i < C::kADma; ++i) {
-        const int r = (wave * C::kADma + i) * 8 + lane / 8;
-        a_off[i] = (uint32_t)min(r, rows - 1) * (uint32_t)ld + (((lane & 7) ^ swz<8>(r)) << 4);
-      }
+      for (int m = 0; m < C::MI; ++m) c.a[m] = (c.a[m] & keep) | (0x7f7f7f7f & ~keep);
 #pragma unroll
-      for (int i = 0; i < C::kBDma; ++i) {
-        const int r = (wave * C::kBDma + i) * 8 + lane / 8;
-        b_off[i] = (uint32_t)min(r, cols - 1) * (uint32_t)ld + (((lane & 7) ^ swz<8>(r)) << 4);
-      }
-      a_c = 0;
-#pragma unroll
-      for (int i = 0; i < C::kSaDma; ++i)
-        sa_off[i] = (uint32_t)min(((wave * C::kSaDma + i) * 64 + lane) % BM, rows - 1) * (uint32_t)g.a_row_mul;
-#pragma unroll
-      for (int i = 0; i < C::kSbDma; ++i)
-        sb_off[i] = (uint32_t)min(((wave * C::kSbDma + i) * 64 + lane) % BN, cols - 1) * (uint32_t)g.b_row_mul;
+      for (int n = 0; n < C::NI; ++n) c.b[n] = (c.b[n] & keep) | (0x7f7f7f7f & ~keep);
     }
-    (void)a_c;
-
-    auto issue = [&](int ks) {
-      const uint32_t st = ring0 + (uint32_t)(ks & 1) * C::kStage;
-      const long long k0 = (long long)ks * C::kRowB;
-      if (ktail && ks == nst - 1) {  // chunks past the row's end repeat the row's first of the stage
+  };
+  auto mma = [&](auto& acc, const Frags& f, const Scales& c, auto step) {
+    constexpr int S = decltype(step)::value;
+    auto wide = [](v4i v) { return v8i{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; };
 #pragma unroll
-        for (int i = 0; i < C::kADma; ++i) {
-          const int r = (wave * C::kADma + i) * 8 + lane / 8;
-          const uint32_t c = ((lane & 7) ^ swz<8>(r)) << 4;
-          dma16(a_base + k0, k0 + c < ld ? a_off[i] : a_off[i] - c, uniform(st + (wave * C::kADma + i) * 1024));
-        }
-#pragma unroll
-        for (int i = 0; i < C::kBDma; ++i) {
-          const int r = (wave * C::kBDma + i) * 8 + lane / 8;
-          const uint32_t c = ((lane & 7) ^ swz<8>(r)) << 4;
-          dma16(b_base + k0, k0 + c < ld ? b_off[i] : b_off[i] - c, uniform(st + C::kA + (wave * C::kBDma + i) * 1024));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < C::kADma; ++i)
-          dma16(a_base + k0, a_off[i], uniform(st + (wave * C::kADma + i) * 1024));
-#pragma unroll
-        for (int i = 0; i < C::kBDma; ++i)
-          dma16(b_base + k0, b_off[i], uniform(st + C::kA + (wave * C::kBDma + i) * 1024));
-      }
-#pragma unroll
-      for (int i = 0; i < C::kSaDma; ++i) {
-        const int t = wave * C::kSaDma + i, j = min(2 * ks + t / (BM / 64), nwords - 1);
-        dma4(sa_base + j * g.a_word_mul, sa_off[i], uniform(st + C::kSA + t * 256));
-      }
-#pragma unroll
-      for (int i = 0; i < C::kSbDma; ++i) {
-        const int t = wave * C::kSbDma + i, j = min(2 * ks + t / (BN / 64), nwords - 1);
-        dma4(sb_base + j * g.b_word_mul, sb_off[i], uniform(st + C::kSB + t * 256));
-      }
-    };
-
-    struct Frags {
-      v4i a[C::MI], b[C::NI];
-    };
-    int sa[C::MI], sb[C::NI];
-    auto load = [&](int ks, int s, Frags& f) {
-      const uint8_t* st = lds + (ks & 1) * C::kStage;
+    for (int n = 0; n < C::NI; ++n)
 #pragma unroll
       for (int m = 0; m < C::MI; ++m)
-        f.a[m] = *reinterpret_cast<const v4i*>(st + (fa ^ (uint32_t)((s << 4) ^ ((m & 1) << 6))) + m * 32 * C::kRowB);
-#pragma unroll
-      for (int n = 0; n < C::NI; ++n)
-        f.b[n] = *reinterpret_cast<const v4i*>(st + (fb ^ (uint32_t)((s << 4) ^ ((n & 1) << 6))) + n * 32 * C::kRowB);
-    };
-    // the last stage's step s, where it lies past K for this lane: zero codes
-    auto cut = [&](int s, Frags& f) {
-      if (ktail && ((nst - 1) * 2 + kb) * 4 + s >= nblk) {
-#pragma unroll
-        for (int m = 0; m < C::MI; ++m) f.a[m] = v4i{0, 0, 0, 0};
-      }
-    };
-    auto load_scales = [&](int ks) {
-      const uint8_t* st = lds + (ks & 1) * C::kStage;
-#pragma unroll
-      for (int m = 0; m < C::MI; ++m) sa[m] = *reinterpret_cast<const int*>(st + wa + m * 128);
-#pragma unroll
-      for (int n = 0; n < C::NI; ++n) sb[n] = *reinterpret_cast<const int*>(st + wb + n * 128);
-    };
-    auto cut_scales = [&]() {  // the last stage's, past K: scales of 1, whatever the padding holds
-      if (ktail) {
-        const int left = nblk - ((nst - 1) * 2 + kb) * 4;
-        const int keep = left >= 4 ? -1 : left <= 0 ? 0 : (1 << (8 * left)) - 1;
-#pragma unroll
-        for (int m = 0; m < C::MI; ++m) sa[m] = (sa[m] & keep) | (0x7f7f7f7f & ~keep);
-#pragma unroll
-        for (int n = 0; n < C::NI; ++n) sb[n] = (sb[n] & keep) | (0x7f7f7f7f & ~keep);
-      }
-    };
-    auto mma = [&](auto& acc, const Frags& f, auto step) {
-      constexpr int S = decltype(step)::value;
-      auto wide = [](v4i v) { return v8i{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; };
-#pragma unroll
-      for (int n = 0; n < C::NI; ++n)
-#pragma unroll
-        for (int m = 0; m < C::MI; ++m)
-          acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(f.b[n]), wide(f.a[m]), acc[m][n], 4, 4, S,
-                                                                      sb[n], S, sa[m]);
-    };
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-    using I2 = std::integral_constant<int, 2>;
-    using I3 = std::integral_constant<int, 3>;
+        acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(f.b[n]), wide(f.a[m]), acc[m][n], 4, 4, S,
+                                                                    c.b[n], S, c.a[m]);
+  };
+  auto mma1 = [&](auto& acc, const Frags& f, const Scales& c, auto step, int i) {  // its i-th instruction
+    constexpr int S = decltype(step)::value;
+    auto wide = [](v4i v) { return v8i{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; };
+    const int n = i / C::MI, m = i % C::MI;
+    acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(f.b[n]), wide(f.a[m]), acc[m][n], 4, 4, S, c.b[n],
+                                                                S, c.a[m]);
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
 
-    __syncthreads();  // every wave is done with the slots (the previous tile's results)
-    issue(0);
-    wait_vm_barrier<0>();
-    if (nst > 1) issue(1);
-    // a wave whose part lies past the group's rows or the columns only moves data
-    const bool live = wm * WTM < rows && wn * WTN < cols;
-    if (!live) {
-      for (int ks = 0; ks + 1 < nst; ++ks) {
-        wait_vm_barrier<0>();
-        if (ks + 2 < nst) issue(ks + 2);
-      }
-      __syncthreads();
-    } else {
+  // loads [lo, hi) of the list above
+  auto issue_range = [&](const Tile& t, int ks, auto lo, auto hi) {
+#pragma unroll
+    for (int i = decltype(lo)::value; i < decltype(hi)::value; ++i) issue(t, i, ks);
+  };
+  constexpr int kCodes = C::kADma + C::kBDma, kBehind = C::kSDma + C::kTouch;
+  using N0 = std::integral_constant<int, 0>;
+  using NCodes = std::integral_constant<int, kCodes>;
+  using NScales = std::integral_constant<int, kCodes + C::kSDma>;
+  using NAll = std::integral_constant<int, C::kPer>;
+  auto start = [&](const Tile& t) {  // codes of stage 0, scales of stages 0 to 2
+    issue_range(t, -2, N0{}, NCodes{});
+#pragma unroll
+    for (int i = 0; i < 3; ++i) issue_range(t, i - 4, NCodes{}, NScales{});
+  };
+  auto second = [&](const Tile& t) {  // codes of stage 1 (of stage 0 again where there is none), scales of stage 3
+    if (nst > 1) issue_range(t, -1, N0{}, NCodes{});
+    issue_range(t, -1, NCodes{}, NScales{});
+    issue_range(t, -1, NScales{}, NAll{});
+  };
+
+  long long p = blockIdx.x >> 3;
+  if (p >= x_cnt) return;
+  Tile t = locate(p);
+  start(t);
+  second(t);
+  for (;;) {
+    const bool more = p + x_step < x_cnt;
+    if (nst > 1) wait_vm_barrier<kCodes + kBehind>();  // the first stage has landed
+    else wait_vm_barrier<0>();
+    Tile next = t;
+    if (wm * WTM < t.rows && wn * WTN < t.cols) {
       v16f acc[C::MI][C::NI];
 #pragma unroll
       for (int m = 0; m < C::MI; ++m)
@@ -374,83 +417,154 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
         for (int n = 0; n < C::NI; ++n)
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.f;
-
       Frags f0, f1;
+      Scales c, c2;
       load(0, 0, f0);
-      load_scales(0);
-      for (int ks = 0; ks + 1 < nst; ++ks) {
-        load(ks, 1, f1);
-        mma(acc, f0, I0{});
-        load(ks, 2, f0);
-        mma(acc, f1, I1{});
-        load(ks, 3, f1);
-        mma(acc, f0, I2{});
-        wait_vm_barrier<0>();
-        if (ks + 2 < nst) issue(ks + 2);
+      load_scales(0, c);
+      // the order of a step: the next step's fragments are asked for, then this one's instructions run.
+      // The scheduler would sink the reads to their use and wait for each
+      auto step = [&](int ks, auto s, Frags& now, Frags& then) {
+        load(ks, decltype(s)::value + 1, then);
+        __builtin_amdgcn_sched_barrier(0);
+        mma(acc, now, c, s);
+        __builtin_amdgcn_sched_barrier(0);
+      };
+#pragma unroll 1
+      for (int ks = 0; ks + 2 < nst; ++ks) {
+        step(ks, I0{}, f0, f1);
+        step(ks, I1{}, f1, f0);
+        step(ks, I2{}, f0, f1);
+        wait_vm_barrier<kBehind>();  // stage ks + 1 has landed
         load(ks + 1, 0, f0);
-        mma(acc, f1, I3{});
-        load_scales(ks + 1);
+        load_scales(ks + 1, c2);
+        __builtin_amdgcn_sched_barrier(0);
+        // the last step's instructions, the loads between them
+        constexpr int kM = C::MI * C::NI;
+#pragma unroll
+        for (int i = 0; i < kM; ++i) {
+          mma1(acc, f1, c, I3{}, i);
+#pragma unroll
+          for (int l = i * C::kPer / kM; l < (i + 1) * C::kPer / kM; ++l) issue(t, l, ks);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        c = c2;
+      }
+      if (nst > 1) {  // the last boundary: nothing more to load
+        const int ks = nst - 2;
+        step(ks, I0{}, f0, f1);
+        step(ks, I1{}, f1, f0);
+        step(ks, I2{}, f0, f1);
+        wait_vm_barrier<0>();
+        load(ks + 1, 0, f0);
+        load_scales(ks + 1, c2);
+        mma(acc, f1, c, I3{});
+        c = c2;
       }
       cut(0, f0);
-      cut_scales();
+      cut_scales(c);
       load(nst - 1, 1, f1);
       cut(1, f1);
-      mma(acc, f0, I0{});
+      mma(acc, f0, c, I0{});
       load(nst - 1, 2, f0);
       cut(2, f0);
-      mma(acc, f1, I1{});
+      mma(acc, f1, c, I1{});
       load(nst - 1, 3, f1);
       cut(3, f1);
-      mma(acc, f0, I2{});
-      mma(acc, f1, I3{});
-      __syncthreads();  // every wave is past its last fragment read
+      mma(acc, f0, c, I2{});
+      mma(acc, f1, c, I3{});
+      wait_vm_barrier<0>();  // every wave is past its last fragment, no load is on its way to a slot
+      if (more) {
+        next = locate(p + x_step);
+        start(next);
+      }
 
-      // lane: row ra + 32 m, columns 8 (i / 4) + 4 kb + i % 4 of column tile n; 256 bytes of each row
-      // at a time, 16-byte chunks swizzled by row
-      constexpr int es = sizeof(T), kPassCols = 256 / es;  // columns per pass
-      constexpr int kPassN = kPassCols / 32;               // column tiles per pass
-      uint8_t* out = lds + wave * (WTM * 256);
+      // lane: row lrow of row tile m, columns 8 q + 4 kb + 0..3 of column tile n; 16-byte chunks swizzled
+      // by row.  The wave's own part of the slot: LDS operations of a wave stay in order
+      // (made from a lane index the compiler cannot see through, or it would keep these addresses in
+      // registers, and then in scratch memory, across the whole K loop)
+      int el = lane;
+      asm volatile("" : "+v"(el));
+      constexpr int es = sizeof(T), kPassCols = 256 / es, kPassN = kPassCols / 32;  // columns, tiles per pass
+      uint8_t* out = lds + C::kSlot + wave * (32 * 256);
+      const int er = el & 31, ekb = el >> 5, ech = el & 15, erow = el >> 4;
+      uint8_t* const put_at = out + er * 256;
+      // 8 loads of 4 rows x 256 bytes: row 4 i + erow, chunk ech ^ (row & 15); (4 i + erow) & 15 has bits 2
+      // and 3 from i
+      const uint8_t* const get_at = out + erow * 256 + (((ech ^ erow) & 3) << 4);
+      const bool full = t.rows == BM && t.cols == BN;
 #pragma unroll
-      for (int h = 0; h < (WTN + kPassCols - 1) / kPassCols; ++h) {
+      for (int m = 0; m < C::MI; ++m)
 #pragma unroll
-        for (int m = 0; m < C::MI; ++m)
+        for (int h = 0; h < (WTN + kPassCols - 1) / kPassCols; ++h) {
 #pragma unroll
           for (int nn = 0; nn < kPassN; ++nn) {
             const int n = h * kPassN + nn;
             if (n < C::NI) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const int r = m * 32 + lrow, at = (nn * 32 + 8 * q + 4 * kb) * es;  // byte in the 256-byte run
+                const int at = (nn * 32 + 8 * q) * es;  // byte of the quarter-wave's run in the 256, kb = 0
                 T v[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = Elem<T>::put(acc[m][n][4 * q + j]);
-                uint8_t* to = out + r * 256 + ((((at >> 4) ^ (r & 15)) << 4) | (at & 15));
+                // 4 kb columns further: es = 2: bit 3 of the byte; es = 4: bit 4
+                uint8_t* to = put_at + (((at + 4 * es * ekb) ^ ((er & 15) << 4)));
                 __builtin_memcpy(__builtin_assume_aligned(to, 4 * es), v, 4 * es);
               }
             }
           }
-        // read back row by row (the wave's own part: no barrier, LDS operations stay in order)
-        const int c = lane & 15;
-        const int col = wn * WTN + h * kPassCols + c * (16 / es);
-#pragma unroll 4
-        for (int r = lane >> 4; r < WTM; r += 4) {
-          Chunk16<es> v;
-          __builtin_memcpy(&v, __builtin_assume_aligned(out + r * 256 + ((c ^ (r & 15)) << 4), 16), 16);
-          if (wm * WTM + r < rows && h * kPassCols + c * (16 / es) < WTN) {
-            T* dst = static_cast<T*>(g.C) + (long long)(row0 + wm * WTM + r) * g.c_stride + n0 + col;
-            if (col + 16 / es <= cols) {
-              *reinterpret_cast<Chunk16<es>*>(dst) = v;
-            } else {
-              T one[16 / es];
-              __builtin_memcpy(one, &v, 16);
+          const int col = wn * WTN + h * kPassCols + ech * (16 / es), row = wm * WTM + m * 32 + erow;
+          T* dst = static_cast<T*>(g.C) + (long long)(t.row0 + row) * g.c_stride + t.n0 + col;
+          const long long step = 4 * g.c_stride;
+          auto chunk = [&](int i) {
+            Chunk16<es> v;
+            __builtin_memcpy(&v, __builtin_assume_aligned(get_at + i * 1024 + (((ech & 12) ^ ((i & 3) << 2)) << 4), 16), 16);
+            return v;
+          };
+          if (full) {
 #pragma unroll
-              for (int j = 0; j < 16 / es; ++j)
-                if (col + j < cols) dst[j] = one[j];
+            for (int i = 0; i < 8; ++i) {
+              *reinterpret_cast<Chunk16<es>*>(dst) = chunk(i);
+              dst += step;
+            }
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              if (row + 4 * i < t.rows) {
+                const Chunk16<es> v = chunk(i);
+                if (col + 16 / es <= t.cols) {
+                  *reinterpret_cast<Chunk16<es>*>(dst) = v;
+                } else {
+                  T one[16 / es];
+                  __builtin_memcpy(one, &v, 16);
+#pragma unroll
+                  for (int j = 0; j < 16 / es; ++j)
+                    if (col + j < t.cols) dst[j] = one[j];
+                }
+              }
+              dst += step;
             }
           }
         }
+    } else {
+      // a wave whose part lies past the group's rows or the columns only moves data: the same loads and
+      // barriers
+#pragma unroll 1
+      for (int ks = 0; ks + 2 < nst; ++ks) {
+        wait_vm_barrier<kBehind>();
+        issue_range(t, ks, N0{}, NAll{});
+      }
+      if (nst > 1) wait_vm_barrier<0>();
+      wait_vm_barrier<0>();
+      if (more) {
+        next = locate(p + x_step);
+        start(next);
       }
     }
+    if (!more) return;
+    __syncthreads();  // the second slot is free
+    second(next);
+    t = next;
+    p += x_step;
   }
 }
 
@@ -482,7 +596,7 @@ static hipError_t launch_tiles(const Mxfp4GemmArgs& g, hipStream_t s) {
 template <typename T>
 static hipError_t launch(const Mxfp4GemmArgs& g, int variant, hipStream_t s) {
   const long long avg = g.rows / g.groups;
-  if (variant == 1 || (variant < 0 && avg > 64)) return launch_tiles<T, 256, 256, 4, 128, 128>(g, s);
+  if (variant == 1 || (variant < 0 && avg > 64)) return launch_tiles<T, 256, 256, 8, 64, 128>(g, s);
   mxfp4_gemm_rows_kernel<T, 4, 2, 2><<<dim3((unsigned)((g.N + 31) / 32), (unsigned)g.groups), 256, 0, s>>>(g);
   return hipGetLastError();
 }
