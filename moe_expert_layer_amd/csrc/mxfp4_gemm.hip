@@ -32,101 +32,108 @@ __device__ __forceinline__ v8i fp4_operand(uint4 q) {
   return v8i{(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
 }
 
-// One group's 16 * NS weight rows against MT * 16 token rows at a time; the NW waves take every
-// NW-th 512-wide stretch of K and their partial sums meet in LDS, in wave order.
-template <typename T, int NW, int NS, int MT>
-__global__ __launch_bounds__(NW * 64) void mxfp4_gemm_rows_kernel(Mxfp4GemmArgs g) {
-  __shared__ float part[NW][MT * 16][NS * 16 + 1];
+// Groups with few rows: the weights are what is read.  One workgroup takes 16 * NS weight rows of one
+// group; its NW waves take every NW-th 512-wide stretch of K, each lane straight from global memory into
+// the matrix instruction's registers (a weight is used once per 16 rows: nothing to gain from LDS), and
+// their partial sums meet in LDS, in wave order.  Rows go 16 or 32 at a time (MT = 1, 2); a group with
+// more is walked again, which the 256-row tiles below do better.
+template <typename T, int NW, int NS, int MAXR, int MT>
+__device__ __forceinline__ void gemm_rows(const Mxfp4GemmArgs& g, float (*part)[MAXR][NS * 16 + 1], int e, int n0, int m0,
+                                          int m_end) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int e = blockIdx.y, n0 = blockIdx.x * (NS * 16);
-  const int2 rr = group_rows(g.offsets, e, g.rows);
   const int r16 = lane & 15, q = lane >> 4;
   const int nblk = g.K / 32, nwords = (nblk + 3) / 4, nst = (nwords + 3) / 4;
   const long long ld = g.K / 2;
-  const uint8_t* bp[NS];
-  const uint8_t* bs[NS];
+  const uint8_t *ap[MT], *as[MT], *bp[NS], *bs[NS];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const long long row = min(m0 + m * 16 + r16, m_end - 1);
+    ap[m] = g.A + row * ld;
+    as[m] = g.A_sf + row * g.a_row_mul;
+  }
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
     const long long row = (long long)e * g.N + min(n0 + s * 16 + r16, g.N - 1);
     bp[s] = g.B + row * ld;
     bs[s] = g.B_sf + row * g.b_row_mul;
   }
-  for (int m0 = rr.x; m0 < rr.y; m0 += MT * 16) {
-    const uint8_t* ap[MT];
-    const uint8_t* as[MT];
+  v4f acc[MT][NS];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) acc[m][s] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int st = wave; st < nst; st += NW) {
+    const int j = st * 4 + q;  // this lane's scale word
+    const int jc = min(j, nwords - 1);
+    const int left = nblk - 4 * j;  // blocks of the word inside K (<= 0: none)
+    int sa[MT], sb[NS];
+    uint4 a[MT][4], b[NS][4];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      sb[s] = *reinterpret_cast<const int*>(bs[s] + (long long)jc * g.b_word_mul);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        b[s][i] = *reinterpret_cast<const uint4*>(bp[s] + (i < left ? (long long)j * 64 + i * 16 : 0));
+    }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const long long row = min(m0 + m * 16 + r16, rr.y - 1);
-      ap[m] = g.A + row * ld;
-      as[m] = g.A_sf + row * g.a_row_mul;
+      sa[m] = *reinterpret_cast<const int*>(as[m] + (long long)jc * g.a_word_mul);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        a[m][i] = *reinterpret_cast<const uint4*>(ap[m] + (i < left ? (long long)j * 64 + i * 16 : 0));
     }
-    v4f acc[MT][NS];
+    if (left < 4) {  // past K: zero codes, and scales of 1 whatever the padding holds
+      const int keep = left <= 0 ? 0 : (1 << (8 * left)) - 1;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m) {
+        sa[m] = (sa[m] & keep) | (0x7f7f7f7f & ~keep);
 #pragma unroll
-      for (int s = 0; s < NS; ++s) acc[m][s] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int st = wave; st < nst; st += NW) {
-      const int j = st * 4 + q;  // this lane's scale word
-      const int jc = min(j, nwords - 1);
-      const int left = nblk - 4 * j;  // blocks of the word inside K (<= 0: none)
-      int sa[MT], sb[NS];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) sa[m] = *reinterpret_cast<const int*>(as[m] + (long long)jc * g.a_word_mul);
-#pragma unroll
-      for (int s = 0; s < NS; ++s) sb[s] = *reinterpret_cast<const int*>(bs[s] + (long long)jc * g.b_word_mul);
-      uint4 a[MT][4], b[NS][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long long at = i < left ? (long long)j * 64 + i * 16 : 0;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) a[m][i] = *reinterpret_cast<const uint4*>(ap[m] + at);
-#pragma unroll
-        for (int s = 0; s < NS; ++s) b[s][i] = *reinterpret_cast<const uint4*>(bp[s] + at);
-      }
-      if (left < 4) {  // past K: zero codes and scales of 1
-        const int keep = left <= 0 ? 0 : (1 << (8 * left)) - 1;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          sa[m] = (sa[m] & keep) | (0x7f7f7f7f & ~keep);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i >= left) a[m][i] = make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int s = 0; s < NS; ++s) sb[s] = (sb[s] & keep) | (0x7f7f7f7f & ~keep);
+        for (int i = 0; i < 4; ++i)
+          if (i >= left) a[m][i] = make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          // the scale byte's index is an immediate
-          acc[m][s] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(a[m][0]), fp4_operand(b[s][0]),
-                                                                       acc[m][s], 4, 4, 0, sa[m], 0, sb[s]);
-          acc[m][s] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(a[m][1]), fp4_operand(b[s][1]),
-                                                                       acc[m][s], 4, 4, 1, sa[m], 1, sb[s]);
-          acc[m][s] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(a[m][2]), fp4_operand(b[s][2]),
-                                                                       acc[m][s], 4, 4, 2, sa[m], 2, sb[s]);
-          acc[m][s] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(a[m][3]), fp4_operand(b[s][3]),
-                                                                       acc[m][s], 4, 4, 3, sa[m], 3, sb[s]);
-        }
+      for (int s = 0; s < NS; ++s) sb[s] = (sb[s] & keep) | (0x7f7f7f7f & ~keep);
     }
-    // lane holds rows 4 q + i, column r16 of each 16 x 16 tile
+    // the scale byte's index is an immediate
+#define MOE_MX_STEP(I)                                                                                            \
+  _Pragma("unroll") for (int s = 0; s < NS; ++s) _Pragma("unroll") for (int m = 0; m < MT; ++m) acc[m][s] =       \
+      __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(a[m][I]), fp4_operand(b[s][I]), acc[m][s], 4, \
+                                                       4, I, sa[m], I, sb[s]);
+    MOE_MX_STEP(0)
+    MOE_MX_STEP(1)
+    MOE_MX_STEP(2)
+    MOE_MX_STEP(3)
+#undef MOE_MX_STEP
+  }
+  // lane holds rows 4 q + i, column r16 of each 16 x 16 tile
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int s = 0; s < NS; ++s)
+    for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[wave][m * 16 + 4 * q + i][s * 16 + r16] = acc[m][s][i];
-    __syncthreads();
-    for (int i = tid; i < MT * 16 * NS * 16; i += NW * 64) {
-      const int r = i / (NS * 16), c = i % (NS * 16);
-      float v = part[0][r][c];
+      for (int i = 0; i < 4; ++i) part[wave][m * 16 + 4 * q + i][s * 16 + r16] = acc[m][s][i];
+  __syncthreads();
+  const int rows = min(MT * 16, m_end - m0);
+  for (int i = tid; i < rows * NS * 16; i += NW * 64) {
+    const int r = i / (NS * 16), c = i % (NS * 16);
+    float v = part[0][r][c];
 #pragma unroll
-      for (int w = 1; w < NW; ++w) v += part[w][r][c];
-      if (m0 + r < rr.y && n0 + c < g.N)
-        static_cast<T*>(g.C)[(long long)(m0 + r) * g.c_stride + n0 + c] = Elem<T>::put(v);
-    }
-    __syncthreads();
+    for (int w = 1; w < NW; ++w) v += part[w][r][c];
+    if (n0 + c < g.N) static_cast<T*>(g.C)[(long long)(m0 + r) * g.c_stride + n0 + c] = Elem<T>::put(v);
+  }
+  __syncthreads();
+}
+
+template <typename T, int NW, int NS, int MAXR>
+__global__ __launch_bounds__(NW * 64) void mxfp4_gemm_rows_kernel(Mxfp4GemmArgs g) {
+  __shared__ float part[NW][MAXR][NS * 16 + 1];
+  const int e = blockIdx.y, n0 = blockIdx.x * (NS * 16);
+  const int2 rr = group_rows(g.offsets, e, g.rows);
+  for (int m0 = rr.x; m0 < rr.y; m0 += MAXR) {
+    const int rows = rr.y - m0;
+    if (rows <= 16) gemm_rows<T, NW, NS, MAXR, 1>(g, part, e, n0, m0, rr.y);
+    else if (MAXR == 32 || rows <= 32) gemm_rows<T, NW, NS, MAXR, 2>(g, part, e, n0, m0, rr.y);
+    else gemm_rows<T, NW, NS, MAXR, MAXR / 16>(g, part, e, n0, m0, rr.y);
   }
 }
 
@@ -143,11 +150,8 @@ __global__ __launch_bounds__(NW * 64) void mxfp4_gemm_rows_kernel(Mxfp4GemmArgs 
 // slot just read) sits before the last step's instructions, when every wave holds its last fragments.
 //
 // Loads of a wave complete in order, so what is issued behind a stage's codes may stay in flight when
-// those are waited for: the scales of two stages further on, and one prefetch.  A prefetch is a 4-byte
-// load whose 64 lanes each touch the line of another row kAhead stages further on, shared out among
-// the workgroups of the XCD that read the same rows, so that the lines are on their way from HBM
-// before the stage's own loads ask the L2 for them.  Loads that have nothing to do (past the last
-// stage) are issued with a buffer of length 0: they read nothing and keep the counts alike.
+// those are waited for: the scales, which are asked for two stages earlier than the codes (every stage
+// takes them from lines of their own, which come from HBM).
 //
 // Weights are the instruction's first operand, so a lane's results are runs of four columns of one
 // row; a wave puts them in type T into its part of the second slot, 32 rows x 256 bytes at a time, and
@@ -158,7 +162,6 @@ __global__ __launch_bounds__(NW * 64) void mxfp4_gemm_rows_kernel(Mxfp4GemmArgs 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-constexpr int kAhead = 1;       // stages between a line's prefetch and its load
 constexpr int kTileGroupN = 8;  // column tiles that go together in the tile order
 
 template <int BM, int BN, int NW, int WTM, int WTN>
@@ -168,13 +171,12 @@ struct TileCfg {
   static constexpr int kSlot = (BM + BN) * kRowB;    // A's rows, then B's
   static constexpr int kScales = 2 * kSlot;          // four slots of [word][A's rows], [word][B's rows]
   static constexpr int kScaleSlot = (BM + BN) * 8;
-  static constexpr int kJunk = kScales + 4 * kScaleSlot, kPlan = kJunk + 256;
+  static constexpr int kPlan = kScales + 4 * kScaleSlot;
   static constexpr int kADma = BM / 8 / NW, kBDma = BN / 8 / NW;  // 1 KB loads per wave and stage
   static constexpr int kSDma = (BM + BN) * 2 / 64 / NW;           // 256-byte loads of scale words
-  static constexpr int kTouch = (BM + BN) / 64 / NW;              // prefetches per wave and stage
-  static constexpr int kPer = kADma + kBDma + kSDma + kTouch;     // loads per wave and stage
+  static constexpr int kPer = kADma + kBDma + kSDma;              // loads per wave and stage
   static_assert(WM * (BN / WTN) == NW && kADma * NW * 8 == BM && kBDma * NW * 8 == BN, "");
-  static_assert(kSDma * NW * 32 == BM + BN && BM % 64 == 0 && BN % 64 == 0 && kTouch >= 1, "");
+  static_assert(kSDma * NW * 32 == BM + BN && BM % 64 == 0 && BN % 64 == 0, "");
   static_assert(NW * 32 * 256 <= kSlot && WTN == 128, "the results' staging fits a slot, in passes of 256 bytes");
 };
 
@@ -225,7 +227,6 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
     const uint8_t* s;          // scale word 0 of the first row of the operand whose scales this wave loads
     uint32_t s_len;
     int row0, rows, n0, cols;
-    uint32_t pf[C::kTouch];    // the rows this lane prefetches, or kNowhere
   };
   auto locate = [&](long long p) {
     const long long L = x_base + p;
@@ -252,13 +253,6 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
     t.b = buffer_srd(g.B + brow * ld, (long long)t.cols * ld);
     t.s = wave * C::kSDma < BM / 32 ? g.A_sf + t.row0 * g.a_row_mul : g.B_sf + brow * g.b_row_mul;
     t.s_len = (uint32_t)(wave * C::kSDma < BM / 32 ? (t.rows - 1) * g.a_row_mul + 4 : (t.cols - 1) * g.b_row_mul + 4);
-    const int share = min(m_tiles, 4);
-#pragma unroll
-    for (int i = 0; i < C::kTouch; ++i) {
-      const int r = (wave * C::kTouch + i) * 64 + lane;  // rows of A, then of B
-      const bool mine = r < BM ? r < t.rows && r % gsz == n : r - BM < t.cols && (r - BM) % share == m % share;
-      t.pf[i] = mine ? (uint32_t)(r < BM ? r : r - BM) * (uint32_t)ld : kNowhere;
-    }
     return t;
   };
 
@@ -286,8 +280,8 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
                       : (uint32_t)(((s_q + i) * 64 + lane) % BN) * (uint32_t)g.b_row_mul;
 
   // load i of this wave for the stages that follow stage ks: codes of stage ks + 2 (past K they are the
-  // next row's, or lie past the buffer; they are cut below), scales of stage ks + 4, lines of stage
-  // ks + 2 + kAhead (of the last stage again where there is none)
+  // next row's, or lie past the buffer; they are cut below), scales of stage ks + 4 (of the last again
+  // where there is none)
   auto issue = [&](const Tile& t, int i, int ks) {
     if (i < C::kADma) {
       dma16_buffer(t.a, a_off[i], (uint32_t)(ks + 2) * C::kRowB,
@@ -296,15 +290,11 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
       const int k = i - C::kADma;
       dma16_buffer(t.b, b_off[k], (uint32_t)(ks + 2) * C::kRowB,
                    ring0 + (uint32_t)(ks & 1) * C::kSlot + BM * C::kRowB + (wave * C::kBDma + k) * 1024);
-    } else if (i < C::kADma + C::kBDma + C::kSDma) {
+    } else {
       const int k = i - C::kADma - C::kBDma, q = wave * C::kSDma + k;
       const int j = min(2 * (ks + 4) + s_word, nwords - 1);
       dma4_buffer(buffer_srd(t.s + j * s_word_mul, t.s_len), s_off[k], 0u,
                   ring0 + C::kScales + (uint32_t)(ks & 3) * C::kScaleSlot + q * 256);
-    } else {
-      const int k = i - C::kADma - C::kBDma - C::kSDma;
-      dma4_buffer((wave * C::kTouch + k) * 64 < BM ? t.a : t.b, t.pf[k], (uint32_t)min(ks + 2 + kAhead, nst - 1) * C::kRowB,
-                  ring0 + C::kJunk);
     }
   };
 
@@ -312,8 +302,8 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
   const int lrow = lane & 31, kb = lane >> 5;
   const int wm = wave % C::WM, wn = wave / C::WM;
   const int ra = wm * WTM + lrow, rb = wn * WTN + lrow;
-  const uint32_t fa = ra * C::kRowB + (((4 * kb) ^ swz<8>(ra)) << 4);
-  const uint32_t fb = (BM + rb) * C::kRowB + (((4 * kb) ^ swz<8>(rb)) << 4);
+  const uint32_t fa_ = ra * C::kRowB + (((4 * kb) ^ swz<8>(ra)) << 4);
+  const uint32_t fb_ = (BM + rb) * C::kRowB + (((4 * kb) ^ swz<8>(rb)) << 4);
   const uint32_t wa = C::kScales + (kb * BM + ra) * 4, wb = C::kScales + (2 * BM + kb * BN + rb) * 4;
 
   struct Frags {
@@ -324,6 +314,8 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
   };
   auto load = [&](int ks, int s, Frags& f) {
     const uint8_t* st = lds + (ks & 1) * C::kSlot;
+    uint32_t fa = fa_, fb = fb_;
+    asm volatile("" : "+v"(fa), "+v"(fb));  // an address is one instruction: made anew rather than kept in registers
 #pragma unroll
     for (int m = 0; m < C::MI; ++m)
       f.a[m] = *reinterpret_cast<const v4i*>(st + (fa ^ (uint32_t)((s << 4) ^ ((m & 1) << 6))) + m * 32 * C::kRowB);
@@ -383,20 +375,18 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
 #pragma unroll
     for (int i = decltype(lo)::value; i < decltype(hi)::value; ++i) issue(t, i, ks);
   };
-  constexpr int kCodes = C::kADma + C::kBDma, kBehind = C::kSDma + C::kTouch;
+  constexpr int kCodes = C::kADma + C::kBDma, kBehind = C::kSDma;
   using N0 = std::integral_constant<int, 0>;
   using NCodes = std::integral_constant<int, kCodes>;
-  using NScales = std::integral_constant<int, kCodes + C::kSDma>;
   using NAll = std::integral_constant<int, C::kPer>;
   auto start = [&](const Tile& t) {  // codes of stage 0, scales of stages 0 to 2
     issue_range(t, -2, N0{}, NCodes{});
 #pragma unroll
-    for (int i = 0; i < 3; ++i) issue_range(t, i - 4, NCodes{}, NScales{});
+    for (int i = 0; i < 3; ++i) issue_range(t, i - 4, NCodes{}, NAll{});
   };
-  auto second = [&](const Tile& t) {  // codes of stage 1 (of stage 0 again where there is none), scales of stage 3
+  auto second = [&](const Tile& t) {  // codes of stage 1, scales of stage 3
     if (nst > 1) issue_range(t, -1, N0{}, NCodes{});
-    issue_range(t, -1, NCodes{}, NScales{});
-    issue_range(t, -1, NScales{}, NAll{});
+    issue_range(t, -1, NCodes{}, NAll{});
   };
 
   long long p = blockIdx.x >> 3;
@@ -491,7 +481,6 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
       // 8 loads of 4 rows x 256 bytes: row 4 i + erow, chunk ech ^ (row & 15); (4 i + erow) & 15 has bits 2
       // and 3 from i
       const uint8_t* const get_at = out + erow * 256 + (((ech ^ erow) & 3) << 4);
-      const bool full = t.rows == BM && t.cols == BN;
 #pragma unroll
       for (int m = 0; m < C::MI; ++m)
 #pragma unroll
@@ -520,10 +509,11 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
             __builtin_memcpy(&v, __builtin_assume_aligned(get_at + i * 1024 + (((ech & 12) ^ ((i & 3) << 2)) << 4), 16), 16);
             return v;
           };
-          if (full) {
+          if (t.cols == BN) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              *reinterpret_cast<Chunk16<es>*>(dst) = chunk(i);
+              const Chunk16<es> v = chunk(i);
+              if (row + 4 * i < t.rows) *reinterpret_cast<Chunk16<es>*>(dst) = v;
               dst += step;
             }
           } else {
@@ -593,12 +583,34 @@ static hipError_t launch_tiles(const Mxfp4GemmArgs& g, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename T, int NW, int NS, int MAXR>
+static hipError_t launch_rows(const Mxfp4GemmArgs& g, hipStream_t s) {
+  mxfp4_gemm_rows_kernel<T, NW, NS, MAXR><<<dim3((unsigned)((g.N + 16 * NS - 1) / (16 * NS)), (unsigned)g.groups), NW * 64, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+// Rows kernel or tiles, by an estimate of both in microseconds from the sizes alone (the groups' rows are on
+// the device: their average stands for them).  The tile kernel takes 8 us a tile plus 1.1 us for each of its
+// stages, in rounds of one tile per CU, however few rows a tile has; the rows kernel's time goes with the
+// multiplications of its 16-row tiles.  Measured, rows / tiles: one group of 8192 x 8192: 64 rows 16 / 44 us,
+// 128 rows 28 / 45 us, 200 rows 47 / 46 us; 8 groups of 4096 x 4096: 32 rows each 20 / 26 us, 64 rows
+// 35 / 27 us; 32 groups of 4096 x 7168: 4 rows each 90 / 99 us, 32 rows 138 / 105 us.
+static bool use_tiles(const Mxfp4GemmArgs& g) {
+  const double avg = (g.rows + g.groups - 1) / g.groups;
+  const double cus = device_cus(), stages = (g.K + 255) / 256;
+  const double tiles = (double)g.groups * ((g.N + 255) / 256) * (double)((int)(avg + 255) / 256);
+  const double tile_us = (double)(long long)((tiles + cus - 1) / cus) * (8.0 + 1.1 * stages);
+  const double rows_us = 5.0 + 3.5e-9 * (double)((int)(avg + 15) / 16 * 16) * g.groups * g.N * g.K;
+  return rows_us > tile_us;
+}
+
 template <typename T>
 static hipError_t launch(const Mxfp4GemmArgs& g, int variant, hipStream_t s) {
-  const long long avg = g.rows / g.groups;
-  if (variant == 1 || (variant < 0 && avg > 64)) return launch_tiles<T, 256, 256, 8, 64, 128>(g, s);
-  mxfp4_gemm_rows_kernel<T, 4, 2, 2><<<dim3((unsigned)((g.N + 31) / 32), (unsigned)g.groups), 256, 0, s>>>(g);
-  return hipGetLastError();
+  if (variant == 1 || (variant < 0 && use_tiles(g))) return launch_tiles<T, 256, 256, 8, 64, 128>(g, s);
+  // up to 16 rows a group: half the registers, twice the waves (32 groups of 7168 x 2048, 4 rows each: 43
+  // against 55 us); above: 64 rows a pass (one group of 8192 x 8192, 64 rows: 16 against 27 us)
+  if ((long long)g.rows <= 16LL * g.groups) return launch_rows<T, 4, 2, 32>(g, s);
+  return launch_rows<T, 4, 2, 64>(g, s);
 }
 
 hipError_t launch_mxfp4_gemm(const Mxfp4GemmArgs& g, int out_dtype, int variant, hipStream_t s) {

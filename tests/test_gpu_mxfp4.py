@@ -208,38 +208,42 @@ PRODUCTS = [  # sizes, N, K
 IDS = [f"G{len(s)}R{sum(s)}N{n}K{k}" for s, n, k in PRODUCTS]
 
 
+@pytest.mark.parametrize("variant", [-1, 0, 1])
 @pytest.mark.parametrize("sizes,N,K", PRODUCTS, ids=IDS)
-def test_product_exact(sizes, N, K):
+def test_product_exact(sizes, N, K, variant):
     """Scales in {1/2, 1, 2}: every product is a multiple of 2^-4 and every sum below 2^20, so float32 sums in any
     order are exact, and so must the results be.  Rows behind the last group stay as they were."""
-    p = Product(sizes, N, K, rows=sum(sizes) + 5, seed=K + N, pad=3, shift=1)
+    p = Product(sizes, N, K, rows=sum(sizes) + 5, seed=K + N, pad=3, shift=1, variant=variant)
     assert torch.equal(p.run().double(), p.ref())
 
 
+@pytest.mark.parametrize("variant", [0, 1])
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("sizes,N,K", PRODUCTS[1:9:2], ids=IDS[1:9:2])
-def test_product_rounding(sizes, N, K, out):
+@pytest.mark.parametrize("sizes,N,K", PRODUCTS[1:9:2] + [([512, 256], 512, 1024)], ids=IDS[1:9:2] + ["whole"])
+def test_product_rounding(sizes, N, K, out, variant):
     """Scales over 2^-7 .. 2^8: K / 64 matrix instructions each round the running sum (at most 2^-23 of the sum of
     magnitudes, whichever way they round), up to 16 partial sums are added, then one rounding to the type."""
-    p = Product(sizes, N, K, lo=116, hi=127, seed=N, out=out)
+    p = Product(sizes, N, K, lo=116, hi=127, seed=N, out=out, variant=variant)
     ref, mag = p.ref(), p.ref(absolute=True)
     t = torch.finfo(DT[out])
     tol = (K / 64 + 17) * 2.0 ** -23 * mag + ref.abs() * t.eps / 2 * (1 + 2.0 ** -10) + t.smallest_normal * t.eps / 2
     assert ((p.run().double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("variant", [0, 1])
 @pytest.mark.parametrize("la", ["rows", "packed"])
 @pytest.mark.parametrize("lb", ["rows", "packed"])
 @pytest.mark.parametrize("sizes,N,K", [([3, 9], 50, 640), ([300, 10], 300, 1152)], ids=["few", "many"])
-def test_product_scale_layouts(sizes, N, K, la, lb):
-    p = Product(sizes, N, K, la=la, lb=lb, seed=2)
+def test_product_scale_layouts(sizes, N, K, la, lb, variant):
+    p = Product(sizes, N, K, la=la, lb=lb, seed=2, variant=variant)
     assert torch.equal(p.run().double(), p.ref())
 
 
+@pytest.mark.parametrize("variant", [0, 1])
 @pytest.mark.parametrize("rows", [7, 600])
-def test_product_nan_scales(rows):
+def test_product_nan_scales(rows, variant):
     """Scale byte 255 makes its row, or its column of its group, NaN, and nothing else."""
-    p = Product([rows, rows], 70, 256, seed=4)
+    p = Product([rows, rows], 70, 256, seed=4, variant=variant)
     p.ab[rows // 2, 3] = 255
     p.bb[70 + 11, 0] = 255
     got, ref = p.run(), p.ref()
@@ -250,21 +254,22 @@ def test_product_nan_scales(rows):
     assert torch.equal(got.double()[~want], ref[~want])
 
 
+@pytest.mark.parametrize("variant", [0, 1])
 @pytest.mark.parametrize("rows", [7, 600])
-def test_product_garbage_past_k(rows):
+def test_product_garbage_past_k(rows, variant):
     """The padding of the last packed scale word is not part of the sum, whatever it holds."""
-    p = Product([rows], 40, 288, seed=9)
+    p = Product([rows], 40, 288, seed=9, variant=variant)
     a, asf, b, bsf, off = p.args()
     for s in (asf, bsf):  # bytes 1 to 3 of the last word lie past K
         s[-1] |= torch.tensor(-256, dtype=torch.int32, device="cuda")  # 0xffffff00
     assert torch.equal(p.run((a, asf, b, bsf, off)).double(), p.ref())
 
 
+@pytest.mark.parametrize("variant", [0, 1])
 @pytest.mark.parametrize("rows", [20, 700])
-def test_product_offsets_are_cut_to_the_rows(rows):
+def test_product_offsets_are_cut_to_the_rows(rows, variant):
     """Offsets outside [0, rows] or descending do not lead outside the tensors."""
-    p = Product([rows], 48, 256, seed=1)
-    p3 = Product([rows, 0, 0], 48, 256, seed=1)
+    p3 = Product([rows, 0, 0], 48, 256, seed=1, variant=variant)
     a, asf, b, bsf, _ = p3.args()
     for off in ([-5, rows // 2, 3, 2 * rows], [0, 1 << 30, 5, -7], [rows, rows + 1, rows + 2, rows + 3]):
         c = torch.full((rows, 48), 77.0, device="cuda")
@@ -277,9 +282,10 @@ def test_product_offsets_are_cut_to_the_rows(rows):
     assert torch.equal(c.cpu().double(), torch.from_numpy(av @ bv[0].T))
 
 
+@pytest.mark.parametrize("variant", [0, 1])
 @pytest.mark.parametrize("rows", [3, 300])
-def test_plain_product_without_offsets(rows):
-    p = Product([rows], 100, 512, seed=6)
+def test_plain_product_without_offsets(rows, variant):
+    p = Product([rows], 100, 512, seed=6, variant=variant)
     a, asf, b, bsf, _ = p.args()
     assert torch.equal(p.run((a, asf, b, bsf, None)).double(), p.ref())
 
