@@ -53,6 +53,13 @@ __device__ __forceinline__ void block_exclusive_scan_2048(int* a) {
   __syncthreads();
 }
 
+// maximum with the DPP-moved lane's value
+template <int CTRL>
+__device__ __forceinline__ uint32_t umax_dpp(uint32_t m) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, CTRL, 0xf, 0xf, false);
+  return m > o ? m : o;
+}
+
 // float32 -> bfloat16 bits, round to nearest even (NaN kept quiet).
 __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
   uint32_t b = __float_as_uint(f);

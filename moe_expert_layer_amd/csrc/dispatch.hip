@@ -41,28 +41,27 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const uint8_t* __restrict
                                                        long long xs_pitch) {
   const int lane = threadIdx.x & 63;
   const long long c0 = ((long long)blockIdx.x * (256 * kDispatchPer) + threadIdx.x) * 16;
+  // the row's last, partial chunk, where it is one of this lane's
+  const long long whole = row_bytes & ~15LL, last = whole == c0 || whole == c0 + 4096 ? whole : row_bytes;
+  static_assert(kDispatchPer == 2, "");
   for (int t = blockIdx.y; t < T; t += gridDim.y) {
     int row;
     uint64_t mask = token_rows(s2r, t, k, max_rows, lane, row);
     if (mask == 0) continue;
     const uint8_t* src = x + (long long)t * x_pitch;
-    Chunk16<1> v[kDispatchPer];
+    u32x4 v[kDispatchPer];
 #pragma unroll
-    for (int i = 0; i < kDispatchPer; ++i) {
-      const long long c = c0 + i * 4096;
-      if (c + 16 <= row_bytes) v[i] = *reinterpret_cast<const Chunk16<1>*>(src + c);
-    }
+    for (int i = 0; i < kDispatchPer; ++i)
+      if (c0 + i * 4096 + 16 <= row_bytes) v[i] = load16(src + c0 + i * 4096);
     while (mask) {
       const int j = __builtin_ctzll(mask);
       mask &= mask - 1;
       uint8_t* dst = xs + (long long)__builtin_amdgcn_readlane(row, j) * xs_pitch;
 #pragma unroll
-      for (int i = 0; i < kDispatchPer; ++i) {
-        const long long c = c0 + i * 4096;
-        if (c + 16 <= row_bytes) *reinterpret_cast<Chunk16<1>*>(dst + c) = v[i];
-        else
-          for (long long b = c; b < row_bytes; ++b) dst[b] = src[b];  // the row's last, partial chunk
-      }
+      for (int i = 0; i < kDispatchPer; ++i)
+        if (c0 + i * 4096 + 16 <= row_bytes) store16(dst + c0 + i * 4096, v[i]);
+      if (last < row_bytes)
+        for (long long b = last; b < row_bytes; ++b) dst[b] = src[b];
     }
   }
 }
@@ -76,7 +75,6 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(const T* __restrict__
                                                            const float* __restrict__ w, int ntok, int k, int max_rows,
                                                            int H, T* __restrict__ y, long long y_stride) {
   constexpr int V = Elem<T>::kVec;
-  using C = Chunk16<sizeof(T)>;
   const int lane = threadIdx.x & 63;
   const int c = (blockIdx.x * 256 + threadIdx.x) * V;
   const bool whole = c + V <= H;
@@ -88,7 +86,7 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(const T* __restrict__
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     while (mask) {
-      const T* src[4];
+      long long src[4];
       float wt[4];
       int n = 0;
 #pragma unroll
@@ -96,20 +94,20 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(const T* __restrict__
         if (mask) {
           const int j = __builtin_ctzll(mask);
           mask &= mask - 1;
-          src[q] = ys + (long long)__builtin_amdgcn_readlane(row, j) * ys_stride + c;
+          src[q] = (long long)__builtin_amdgcn_readlane(row, j) * ys_stride + c;
           wt[q] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wl), j));
           n = q + 1;
         }
       if (whole) {
-        C v[4];
+        u32x4 v[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (q < n) v[q] = *reinterpret_cast<const C*>(src[q]);
+          if (q < n) v[q] = load16(ys + src[q]);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           if (q < n) {
             float f[V];
-            Elem<T>::unpack(v[q].w, f);
+            Elem<T>::unpack(v[q], f);
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[i] = WEIGHTED ? fmaf(wt[q], f[i], acc[i]) : acc[i] + f[i];
           }
@@ -118,16 +116,14 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(const T* __restrict__
 #pragma unroll
           for (int i = 0; i < V; ++i)
             if (c + i < H) {
-              const float f = Elem<T>::get(src[q][i]);
+              const float f = Elem<T>::get(ys[src[q] + i]);
               acc[i] = WEIGHTED ? fmaf(wt[q], f, acc[i]) : acc[i] + f;
             }
       }
     }
     T* dst = y + (long long)t * y_stride + c;
     if (whole) {
-      C o;
-      pack16<T>(acc, o.w);
-      *reinterpret_cast<C*>(dst) = o;
+      store16(dst, pack16<T>(acc));
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -151,7 +147,6 @@ __global__ __launch_bounds__(NW * 64) void combine_backward_kernel(
     const int32_t* __restrict__ s2r, const float* __restrict__ w, int ntok, int k, int max_rows, int H,
     T* __restrict__ dys, float* __restrict__ dw, const int32_t* __restrict__ ids, int E, float* __restrict__ dlogits) {
   constexpr int V = Elem<T>::kVec, U = 4;  // chunks in flight per lane
-  using C = Chunk16<sizeof(T)>;
   __shared__ float part[16][NW];  // [slot][wave of its group]
   __shared__ float g[16];
   __shared__ int gid[16];
@@ -175,13 +170,13 @@ __global__ __launch_bounds__(NW * 64) void combine_backward_kernel(
       T* dst = dys + r * row_stride;
       float dot = 0.f;
       for (int c0 = p * 64 + lane; c0 < nchunk; c0 += P * 64 * U) {
-        C a[U], b[U];
+        u32x4 a[U], b[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int c = c0 + u * P * 64;
           if (c < nchunk) {
-            a[u] = *reinterpret_cast<const C*>(dyt + (long long)c * V);
-            b[u] = *reinterpret_cast<const C*>(src + (long long)c * V);
+            a[u] = load16(dyt + (long long)c * V);
+            b[u] = load16(src + (long long)c * V);
           }
         }
 #pragma unroll
@@ -189,16 +184,14 @@ __global__ __launch_bounds__(NW * 64) void combine_backward_kernel(
           const int c = c0 + u * P * 64;
           if (c < nchunk) {
             float fa[V], fb[V], o[V];
-            Elem<T>::unpack(a[u].w, fa);
-            Elem<T>::unpack(b[u].w, fb);
+            Elem<T>::unpack(a[u], fa);
+            Elem<T>::unpack(b[u], fb);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
               dot = fmaf(fa[i], fb[i], dot);
               o[i] = wt * fa[i];
             }
-            C ov;
-            pack16<T>(o, ov.w);
-            *reinterpret_cast<C*>(dst + (long long)c * V) = ov;
+            store16(dst + (long long)c * V, pack16<T>(o));
           }
         }
       }

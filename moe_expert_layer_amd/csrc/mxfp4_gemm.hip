@@ -505,24 +505,22 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
           T* dst = static_cast<T*>(g.C) + (long long)(t.row0 + row) * g.c_stride + t.n0 + col;
           const long long step = 4 * g.c_stride;
           auto chunk = [&](int i) {
-            Chunk16<es> v;
-            __builtin_memcpy(&v, __builtin_assume_aligned(get_at + i * 1024 + (((ech & 12) ^ ((i & 3) << 2)) << 4), 16), 16);
-            return v;
+            return *reinterpret_cast<const u32x4*>(get_at + i * 1024 + (((ech & 12) ^ ((i & 3) << 2)) << 4));
           };
           if (t.cols == BN) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const Chunk16<es> v = chunk(i);
-              if (row + 4 * i < t.rows) *reinterpret_cast<Chunk16<es>*>(dst) = v;
+              const u32x4 v = chunk(i);
+              if (row + 4 * i < t.rows) store16(dst, v);
               dst += step;
             }
           } else {
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) {
               if (row + 4 * i < t.rows) {
-                const Chunk16<es> v = chunk(i);
+                const u32x4 v = chunk(i);
                 if (col + 16 / es <= t.cols) {
-                  *reinterpret_cast<Chunk16<es>*>(dst) = v;
+                  store16(dst, v);
                 } else {
                   T one[16 / es];
                   __builtin_memcpy(one, &v, 16);
@@ -609,7 +607,12 @@ static hipError_t launch(const Mxfp4GemmArgs& g, int variant, hipStream_t s) {
   if (variant == 1 || (variant < 0 && use_tiles(g))) return launch_tiles<T, 256, 256, 8, 64, 128>(g, s);
   // up to 16 rows a group: half the registers, twice the waves (32 groups of 7168 x 2048, 4 rows each: 43
   // against 55 us); above: 64 rows a pass (one group of 8192 x 8192, 64 rows: 16 against 27 us)
-  if ((long long)g.rows <= 16LL * g.groups) return launch_rows<T, 4, 2, 32>(g, s);
+  if ((long long)g.rows <= 16LL * g.groups) {
+    // fewer workgroups than CUs: half the columns, eight waves along K (one row, 4099 x 7168: 5.6 against
+    // 7.3 us; one group of 8192 x 8192, which has enough: 12.2 against 10.0 us)
+    if ((long long)g.groups * ((g.N + 31) / 32) < device_cus()) return launch_rows<T, 8, 1, 32>(g, s);
+    return launch_rows<T, 4, 2, 32>(g, s);
+  }
   return launch_rows<T, 4, 2, 64>(g, s);
 }
 

@@ -18,12 +18,6 @@
 
 namespace moe {
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t umax_dpp(uint32_t m) {
-  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, CTRL, 0xf, 0xf, false);
-  return m > o ? m : o;
-}
-
 __global__ __launch_bounds__(256) void quantize_act_kernel(const uint4* __restrict__ x, long long n8,
                                                            uint2* __restrict__ q, uint8_t* __restrict__ sf) {
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // group of 8 values
