@@ -322,7 +322,7 @@ moe_status moe_unpack_scales(int32_t rows, int32_t groups, const int32_t* packed
  *     topk_w, dw [T, k] and dlogits [T, E_tot] are float32 and dense, topk_ids int32 [T, k].
  *   - Sums are taken in float32 in slot order and rounded once (to nearest even) to the dtype;
  *     there are no atomics, so results are the same from run to run.  A slot without a row is
- *     left out (its weight is not read as 0 times something); a row with a weight of 0 is read.
+ *     left out of the sums whatever its weight; a row with a weight of 0 is read (0 * NaN = NaN).
  *   - Rows that no slot owns, and the elements between H and the stride, are left as they were.
  *   - slot_to_row comes from moe_sort_tokens or moe_route_permute; a map entry outside
  *     [0, max_rows) counts as no row, so rows past the caller's tensors are dropped.  Two slots
@@ -330,7 +330,7 @@ moe_status moe_unpack_scales(int32_t rows, int32_t groups, const int32_t* packed
  *   - Pointers are aligned to their element; outputs must not overlap inputs or each other.
  *     Stream, validation and error rules are those at the top of this file.  num_tokens = 0
  *     launches nothing.
- *   - Limits: 1 <= H <= 2^20; 1 <= E_loc <= E_tot <= 1024; 1 <= k <= 16; T*k < 2^31; strides
+ *   - Limits: 1 <= H <= 2^20; 1 <= E_loc <= E_tot <= 1024; 1 <= k <= 16; T*k <= 2^31 - 2^17; strides
  *     0 (= H) or H to 2^40; max_rows 0 (= T*k) to T*k. */
 
 /* Element types of the tensors below. */
@@ -430,11 +430,11 @@ typedef struct {
  *   c[r, n] = sum_k a[r, k] * b[e, n, k]   for offsets[e] <= r < offsets[e + 1]
  * a [rows, K] (say, quantised tokens in expert order), b [groups, N, K], offsets int32
  * [groups + 1] on the device, ascending from 0 (moe_sort_tokens), or NULL with one group: all rows
- * (a plain product).  Rows at or past offsets[groups] are neither read nor written; offsets outside
- * [0, rows] or descending are cut to it.  The sum's order depends on the sizes only, so results
- * are the same from run to run.  a, b and row-major scales 16-byte aligned, packed scales 4-byte,
- * c aligned to its element; c must not overlap the inputs.  No workspace.  Scale byte 255 makes
- * every result that reads it NaN.  Errors as for the other calls; MOE_ERR_UNSUPPORTED for
+ * (a plain product).  Rows of c at or past offsets[groups] are left as they were.  Offsets outside
+ * [0, rows] or descending give unspecified results, but no access outside the tensors.  The sum's
+ * order depends on the sizes only, so results are the same from run to run.  a and b 16-byte
+ * aligned, scales 4-byte, c to its element; c must not overlap the inputs.  No workspace.  Scale
+ * byte 255 makes every result that reads it NaN.  Errors as for the other calls; MOE_ERR_UNSUPPORTED for
  * row-major scales with K not a multiple of 128 (moe_pack_scales packs them). */
 moe_status moe_mxfp4_gemm(const moe_mxfp4_gemm_desc* desc, const uint8_t* a, const void* a_sf, const uint8_t* b,
                           const void* b_sf, const int32_t* offsets, void* c, void* stream);

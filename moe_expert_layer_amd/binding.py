@@ -255,25 +255,27 @@ def _refuse(status: int, msg: str):
 def _rows_tensor(name, t, dtype, rows, cols, stride, dev, at_least=False):
     """A [rows, cols] tensor of dtype on device dev whose rows lie stride elements apart (at_least: it
     may have more rows)."""
-    if t.dtype is not dtype:
-        _refuse(MOE_ERR_INVALID_DESC, f"{name} is {t.dtype}, not {dtype}")
-    if t.get_device() != dev:
-        _refuse(MOE_ERR_UNSUPPORTED, f"{name} is not on the GPU of the other tensors")
-    sh, st = t.shape, t.stride()
-    if len(sh) != 2 or sh[1] != cols or (sh[0] < rows if at_least else sh[0] != rows):
-        _refuse(MOE_ERR_INVALID_DESC, f"{name} has shape {tuple(sh)}, not ({rows}, {cols})")
+    sh = t.shape
+    if t.dtype is not dtype or t.get_device() != dev or len(sh) != 2 or sh[1] != cols or (
+            sh[0] < rows if at_least else sh[0] != rows):
+        _refuse_tensor(name, t, dtype, dev, f"({rows}, {cols})")
+    st = t.stride()
     if (st[1] != 1 and cols > 1) or (st[0] != stride and rows > 1):
         _refuse(MOE_ERR_INVALID_DESC, f"{name} has strides {st}, not ({stride}, 1)")
 
 
 def _array(name, t, dtype, n, dev):
     """A dense tensor of dtype with at least n elements on device dev."""
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+        _refuse_tensor(name, t, dtype, dev, f"{n} elements, contiguous")
+
+
+def _refuse_tensor(name, t, dtype, dev, wanted):
     if t.dtype is not dtype:
         _refuse(MOE_ERR_INVALID_DESC, f"{name} is {t.dtype}, not {dtype}")
     if t.get_device() != dev:
         _refuse(MOE_ERR_UNSUPPORTED, f"{name} is not on the GPU of the other tensors")
-    if t.numel() < n or not t.is_contiguous():
-        _refuse(MOE_ERR_INVALID_DESC, f"{name} holds {t.numel()} elements (contiguous: {t.is_contiguous()}), needs {n}")
+    _refuse(MOE_ERR_INVALID_DESC, f"{name} has shape {tuple(t.shape)} and strides {t.stride()}, not {wanted}")
 
 
 def _device_of(t) -> int:
@@ -283,34 +285,51 @@ def _device_of(t) -> int:
     return dev
 
 
+class _Torch:
+    """What the calls below need of torch, looked up once (torch is imported with the first call, not with this module)."""
+
+    def __init__(self):
+        import torch
+        self.raw_stream, self.current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        self.device = torch.cuda.device
+        self.i32, self.f32, self.u8 = torch.int32, torch.float32, torch.uint8
+        self.dtypes = {MOE_DT_BF16: torch.bfloat16, MOE_DT_F16: torch.float16, MOE_DT_F32: torch.float32,
+                       MOE_DT_U8: torch.uint8}
+
+
+_torch_names = None
+
+
+def _torch() -> _Torch:
+    global _torch_names
+    if _torch_names is None:
+        _torch_names = _Torch()
+    return _torch_names
+
+
 def _launch(fn, dev: int, stream, *args):
     """fn(*args, stream) with device dev current, on its current stream unless one is given."""
-    import torch
+    T = _torch()
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
+        raw = T.raw_stream(dev)
     else:
         if stream.device.index != dev:
             _refuse(MOE_ERR_UNSUPPORTED, f"stream of GPU {stream.device.index}, tensors on GPU {dev}")
         raw = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        _check(fn(*args, raw))
+    if T.current() == dev:
+        st = fn(*args, raw)
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, raw))
-
-
-_TORCH_DTYPES = None
+        with T.device(dev):
+            st = fn(*args, raw)
+    if st:
+        _check(st)
 
 
 def _torch_dtype(dtype: int):
-    global _TORCH_DTYPES
-    if _TORCH_DTYPES is None:
-        import torch
-        _TORCH_DTYPES = {MOE_DT_BF16: torch.bfloat16, MOE_DT_F16: torch.float16, MOE_DT_F32: torch.float32,
-                         MOE_DT_U8: torch.uint8}
-    if dtype not in _TORCH_DTYPES:
+    t = _torch().dtypes.get(dtype)
+    if t is None:
         _refuse(MOE_ERR_INVALID_DESC, f"dtype {dtype} unknown")
-    return _TORCH_DTYPES[dtype]
+    return t
 
 
 def make_dispatch_desc(num_tokens: int, hidden: int, num_experts: int, topk: int, local_begin: int = 0,
@@ -335,58 +354,80 @@ def alloc_sort_workspace(desc: MoeDispatchDesc, device="cuda"):
     return torch.empty(max(moe_sort_workspace_size(desc), 256), dtype=torch.uint8, device=device)
 
 
-def _token_tensor(name, d, t, dev):
-    _rows_tensor(name, t, _torch_dtype(d.dtype), d.num_tokens, d.hidden, d.token_stride or d.hidden, dev)
+class _DispatchView:
+    """A dispatch descriptor's fields as the checks below want them."""
+
+    def __init__(self, d):
+        T = _torch()
+        self.i32, self.f32, self.u8, self.dtype = T.i32, T.f32, T.u8, _torch_dtype(d.dtype)
+        self.slots, self.hidden, self.num_local = d.num_tokens * d.topk, d.hidden, d.num_local
+        self.logits = d.num_tokens * d.num_experts
+        self.tokens, self.rows = (d.num_tokens, d.hidden), (d.max_rows or self.slots, d.hidden)
+        self.token_stride, self.row_stride = (d.token_stride or d.hidden, 1), (d.row_stride or d.hidden, 1)
+
+    def token_tensor(self, name, t, dev):
+        # the usual case in one line, every other one (a single row or column, a fault) by the book
+        if t.dtype is not self.dtype or t.get_device() != dev or t.shape != self.tokens or t.stride() != self.token_stride:
+            _rows_tensor(name, t, self.dtype, *self.tokens, self.token_stride[0], dev)
+
+    def expert_tensor(self, name, t, dev):
+        if t.dtype is not self.dtype or t.get_device() != dev or t.shape != self.rows or t.stride() != self.row_stride:
+            _rows_tensor(name, t, self.dtype, *self.rows, self.row_stride[0], dev, at_least=True)
 
 
-def _expert_tensor(name, d, t, dev):
-    _rows_tensor(name, t, _torch_dtype(d.dtype), d.max_rows or d.num_tokens * d.topk, d.hidden,
-                 d.row_stride or d.hidden, dev, at_least=True)
+_views = {}  # descriptor bytes -> _DispatchView: a descriptor may change between calls, its bytes say whether it did
+
+
+def _view(desc) -> _DispatchView:
+    key = bytes(desc)
+    v = _views.get(key)
+    if v is None:
+        if len(_views) >= 1024:
+            _views.clear()
+        v = _views[key] = _DispatchView(desc)
+    return v
 
 
 def moe_sort_tokens(desc, topk_ids, counts, offsets, row_to_slot, slot_to_row, workspace, stream=None):
     """Expert ids int32 [T, k] -> counts, offsets, row_to_slot, slot_to_row (int32), as moe_route_permute writes them."""
-    import torch
-    dev, n, i32 = _device_of(topk_ids), desc.num_tokens * desc.topk, torch.int32
+    v, dev = _view(desc), _device_of(topk_ids)
+    n, i32 = v.slots, v.i32
     _array("topk_ids", topk_ids, i32, n, dev)
-    _array("counts", counts, i32, desc.num_local, dev)
-    _array("offsets", offsets, i32, desc.num_local + 1, dev)
+    _array("counts", counts, i32, v.num_local, dev)
+    _array("offsets", offsets, i32, v.num_local + 1, dev)
     _array("row_to_slot", row_to_slot, i32, n, dev)
     _array("slot_to_row", slot_to_row, i32, n, dev)
-    _array("workspace", workspace, torch.uint8, 0, dev)
+    _array("workspace", workspace, v.u8, 0, dev)
     _launch(lib().moe_sort_tokens, dev, stream, ctypes.byref(desc), topk_ids.data_ptr(), counts.data_ptr(),
             offsets.data_ptr(), row_to_slot.data_ptr(), slot_to_row.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def moe_dispatch(desc, x, slot_to_row, xs, stream=None):
     """Token rows x [T, H] -> expert-ordered rows xs [max_rows, H] (rows that no slot owns are left as they were)."""
-    import torch
-    dev = _device_of(x)
-    _token_tensor("x", desc, x, dev)
-    _array("slot_to_row", slot_to_row, torch.int32, desc.num_tokens * desc.topk, dev)
-    _expert_tensor("xs", desc, xs, dev)
+    v, dev = _view(desc), _device_of(x)
+    v.token_tensor("x", x, dev)
+    _array("slot_to_row", slot_to_row, v.i32, v.slots, dev)
+    v.expert_tensor("xs", xs, dev)
     _launch(lib().moe_dispatch, dev, stream, ctypes.byref(desc), x.data_ptr(), slot_to_row.data_ptr(), xs.data_ptr())
 
 
 def moe_dispatch_backward(desc, dxs, slot_to_row, dx, stream=None):
     """Gradient of moe_dispatch: dx[t] = the sum of the rows of dxs that token t went to."""
-    import torch
-    dev = _device_of(dxs)
-    _expert_tensor("dxs", desc, dxs, dev)
-    _array("slot_to_row", slot_to_row, torch.int32, desc.num_tokens * desc.topk, dev)
-    _token_tensor("dx", desc, dx, dev)
+    v, dev = _view(desc), _device_of(dxs)
+    v.expert_tensor("dxs", dxs, dev)
+    _array("slot_to_row", slot_to_row, v.i32, v.slots, dev)
+    v.token_tensor("dx", dx, dev)
     _launch(lib().moe_dispatch_backward, dev, stream, ctypes.byref(desc), dxs.data_ptr(), slot_to_row.data_ptr(),
             dx.data_ptr())
 
 
 def moe_combine(desc, ys, slot_to_row, topk_w, y, stream=None):
     """Expert-ordered rows ys -> y[t] = sum_j topk_w[t, j] * ys[slot_to_row[t, j]], in token order."""
-    import torch
-    dev, n = _device_of(ys), desc.num_tokens * desc.topk
-    _expert_tensor("ys", desc, ys, dev)
-    _array("slot_to_row", slot_to_row, torch.int32, n, dev)
-    _array("topk_w", topk_w, torch.float32, n, dev)
-    _token_tensor("y", desc, y, dev)
+    v, dev = _view(desc), _device_of(ys)
+    v.expert_tensor("ys", ys, dev)
+    _array("slot_to_row", slot_to_row, v.i32, v.slots, dev)
+    _array("topk_w", topk_w, v.f32, v.slots, dev)
+    v.token_tensor("y", y, dev)
     _launch(lib().moe_combine, dev, stream, ctypes.byref(desc), ys.data_ptr(), slot_to_row.data_ptr(),
             topk_w.data_ptr(), y.data_ptr())
 
@@ -394,18 +435,17 @@ def moe_combine(desc, ys, slot_to_row, topk_w, y, stream=None):
 def moe_combine_backward(desc, dy, ys, slot_to_row, topk_w, dys, dw, topk_ids=None, dlogits=None, stream=None):
     """Gradients of moe_combine: dys (rows), dw [T, k] float32 and, where dlogits [T, E_tot] float32 is given
     (with topk_ids), the gradient of the routing logits under the softmax over the chosen ones."""
-    import torch
-    dev, n = _device_of(dy), desc.num_tokens * desc.topk
-    _token_tensor("dy", desc, dy, dev)
-    _expert_tensor("ys", desc, ys, dev)
-    _array("slot_to_row", slot_to_row, torch.int32, n, dev)
-    _array("topk_w", topk_w, torch.float32, n, dev)
-    _expert_tensor("dys", desc, dys, dev)
-    _array("dw", dw, torch.float32, n, dev)
+    v, dev = _view(desc), _device_of(dy)
+    v.token_tensor("dy", dy, dev)
+    v.expert_tensor("ys", ys, dev)
+    _array("slot_to_row", slot_to_row, v.i32, v.slots, dev)
+    _array("topk_w", topk_w, v.f32, v.slots, dev)
+    v.expert_tensor("dys", dys, dev)
+    _array("dw", dw, v.f32, v.slots, dev)
     if topk_ids is not None:
-        _array("topk_ids", topk_ids, torch.int32, n, dev)
+        _array("topk_ids", topk_ids, v.i32, v.slots, dev)
     if dlogits is not None:
-        _array("dlogits", dlogits, torch.float32, desc.num_tokens * desc.num_experts, dev)
+        _array("dlogits", dlogits, v.f32, v.logits, dev)
     _launch(lib().moe_combine_backward, dev, stream, ctypes.byref(desc), dy.data_ptr(), ys.data_ptr(),
             slot_to_row.data_ptr(), topk_w.data_ptr(), dys.data_ptr(), dw.data_ptr(), _ptr(topk_ids), _ptr(dlogits))
 
@@ -426,12 +466,12 @@ def make_mxfp4_gemm_desc(rows: int, n: int, k: int, groups: int = 1, out_dtype: 
 
 
 def _codes_and_scales(name, codes, sf, rows, k, layout, dev):
-    import torch
-    _array(name, codes, torch.uint8, rows * (k // 2), dev)
+    T = _torch()
+    _array(name, codes, T.u8, rows * (k // 2), dev)
     if layout == MOE_SF_PACKED_MN:
-        _array(name + "_sf", sf, torch.int32, (k // 32 + 3) // 4 * ((rows + 3) // 4 * 4), dev)
+        _array(name + "_sf", sf, T.i32, (k // 32 + 3) // 4 * ((rows + 3) // 4 * 4), dev)
     else:
-        _array(name + "_sf", sf, torch.uint8, rows * (k // 32), dev)
+        _array(name + "_sf", sf, T.u8, rows * (k // 32), dev)
 
 
 def moe_quantize_mxfp4(desc, values, codes, sf, stream=None):
@@ -456,12 +496,12 @@ def moe_dequantize_mxfp4(desc, codes, sf, values, dtype: Optional[str] = None, s
 def moe_mxfp4_gemm(desc, a, a_sf, b, b_sf, offsets, c, stream=None):
     """c[r] = a[r] @ b[e].T for the rows of each group e (offsets int32 [groups + 1]; None: one group of all rows);
     a, b: E2M1 codes with their scales, c [rows, n].  Rows past the last group are left as they were."""
-    import torch
+    T = _torch()
     dev = _device_of(a)
     _codes_and_scales("a", a, a_sf, desc.rows, desc.k, desc.a_scale_layout, dev)
     _codes_and_scales("b", b, b_sf, desc.groups * desc.n, desc.k, desc.b_scale_layout, dev)
     if offsets is not None:
-        _array("offsets", offsets, torch.int32, desc.groups + 1, dev)
+        _array("offsets", offsets, T.i32, desc.groups + 1, dev)
     _rows_tensor("c", c, _torch_dtype(desc.out_dtype), desc.rows, desc.n, desc.out_stride or desc.n, dev)
     _launch(lib().moe_mxfp4_gemm, dev, stream, ctypes.byref(desc), a.data_ptr(), a_sf.data_ptr(), b.data_ptr(),
             b_sf.data_ptr(), _ptr(offsets), c.data_ptr())

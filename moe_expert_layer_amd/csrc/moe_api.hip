@@ -485,6 +485,7 @@ namespace {
 
 constexpr int kMaxDispatchHidden = 1 << 20;
 constexpr long long kMaxStride = 1LL << 40;
+constexpr long long kMaxSlots = (1LL << 31) - (1LL << 17);
 
 moe_status check_dispatch_desc(const moe_dispatch_desc* d) {
   if (!d) return fail(MOE_ERR_NULL, "desc is NULL");
@@ -499,7 +500,8 @@ moe_status check_dispatch_desc(const moe_dispatch_desc* d) {
   if (d->topk < 1 || d->topk > moe::kMaxTopk)
     return fail(MOE_ERR_INVALID_DESC, "topk %d outside [1, %d]", d->topk, moe::kMaxTopk);
   const long long slots = (long long)d->num_tokens * d->topk;
-  if (slots >= (1LL << 31)) return fail(MOE_ERR_INVALID_DESC, "num_tokens * topk must be < 2^31");
+  // the kernels step through slots and tokens in 32 bits, up to a grid of 65535 tokens past the last
+  if (slots > kMaxSlots) return fail(MOE_ERR_INVALID_DESC, "num_tokens * topk must be at most 2^31 - 2^17");
   if (d->dtype < MOE_DT_BF16 || d->dtype > MOE_DT_U8) return fail(MOE_ERR_INVALID_DESC, "dtype %d unknown", d->dtype);
   if (d->max_rows < 0 || d->max_rows > slots)
     return fail(MOE_ERR_INVALID_DESC, "max_rows %d outside [0, num_tokens * topk]", d->max_rows);
@@ -716,8 +718,7 @@ moe_status moe_mxfp4_gemm(const moe_mxfp4_gemm_desc* d, const uint8_t* a, const 
   if (d->rows == 0) return ok();
   if (!a || !a_sf || !b || !b_sf || !c) return fail(MOE_ERR_NULL, "a/a_sf/b/b_sf/c NULL");
   if (!offsets && d->groups != 1) return fail(MOE_ERR_NULL, "offsets NULL with %d groups", d->groups);
-  if (misaligned(a, 16) || misaligned(b, 16) || misaligned(a_sf, d->a_scale_layout == MOE_SF_PACKED_MN ? 4 : 16) ||
-      misaligned(b_sf, d->b_scale_layout == MOE_SF_PACKED_MN ? 4 : 16) || misaligned(offsets, 4) ||
+  if (misaligned(a, 16) || misaligned(b, 16) || misaligned(a_sf, 4) || misaligned(b_sf, 4) || misaligned(offsets, 4) ||
       misaligned(c, (size_t)moe::dtype_bytes(d->out_dtype)))
     return fail(MOE_ERR_MISALIGNED, "a / a_sf / b / b_sf / offsets / c misaligned");
   if (moe_status st = check_device()) return st;

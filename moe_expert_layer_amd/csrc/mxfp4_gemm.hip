@@ -184,16 +184,18 @@ template <typename T, int BM, int BN, int NW, int WTM, int WTN>
 __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmArgs g) {
   using C = TileCfg<BM, BN, NW, WTM, WTN>;
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  int* s_plan = reinterpret_cast<int*>(lds + C::kPlan);  // [groups + 1] first row tile of each group
-  int* s_lo = s_plan + g.groups + 1;                     // [groups] first row
-  int* s_hi = s_lo + g.groups;                           // [groups] end
-  int* s_wsum = s_hi + g.groups;                         // [NW]
+  // the first row tile of each group [groups + 1], unsigned: groups that overlap (offsets that are not
+  // what they should be) have at most 1024 * 2^22 tiles
+  unsigned* s_plan = reinterpret_cast<unsigned*>(lds + C::kPlan);
+  int* s_lo = reinterpret_cast<int*>(s_plan + g.groups + 1);  // [groups] first row
+  int* s_hi = s_lo + g.groups;                                // [groups] end
+  unsigned* s_wsum = reinterpret_cast<unsigned*>(s_hi + g.groups);  // [NW]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   {  // the plan, by a scan over the groups
     const int per = (g.groups + C::NT - 1) / C::NT, beg = tid * per;
-    int sum = 0;
+    unsigned sum = 0;
     for (int i = beg; i < min(beg + per, g.groups); ++i) {
       const int2 r = group_rows(g.offsets, i, g.rows);
       s_lo[i] = r.x;
@@ -201,10 +203,10 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
       s_plan[i] = sum;
       sum += (r.y - r.x + BM - 1) / BM;
     }
-    const int inc = wave_inclusive_scan(sum);
+    const unsigned inc = (unsigned)wave_inclusive_scan((int)sum);
     if (lane == 63) s_wsum[wave] = inc;
     __syncthreads();
-    int base = inc - sum;
+    unsigned base = inc - sum;
     for (int w = 0; w < wave; ++w) base += s_wsum[w];
     for (int i = beg; i < min(beg + per, g.groups); ++i) s_plan[i] += base;
     if (tid == C::NT - 1) s_plan[g.groups] = base + sum;
@@ -231,14 +233,14 @@ __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmAr
   auto locate = [&](long long p) {
     const long long L = x_base + p;
     int e = 0, hi = g.groups - 1;
-    const int mt = (int)(L / n_tiles);
+    const unsigned mt = (unsigned)(L / n_tiles);
     while (e < hi) {  // the last group that starts at or before this row tile (it has rows)
       const int mid = (e + hi + 1) >> 1;
       if (s_plan[mid] <= mt) e = mid; else hi = mid - 1;
     }
     e = __builtin_amdgcn_readfirstlane(e);
-    const int first = __builtin_amdgcn_readfirstlane(s_plan[e]);
-    const int m_tiles = __builtin_amdgcn_readfirstlane(s_plan[e + 1]) - first;
+    const unsigned first = __builtin_amdgcn_readfirstlane(s_plan[e]);
+    const int m_tiles = (int)(__builtin_amdgcn_readfirstlane(s_plan[e + 1]) - first);
     const int li = (int)(L - (long long)first * n_tiles);
     const int grp = li / (kTileGroupN * m_tiles);
     const int gsz = min(n_tiles - grp * kTileGroupN, kTileGroupN);

@@ -24,7 +24,7 @@ def desc(**kw):
 
 BAD = [("num_tokens", -1), ("hidden", 0), ("hidden", (1 << 20) + 1), ("num_experts", 0), ("num_experts", 1025),
        ("num_local", 0), ("num_local", 9), ("local_begin", -1), ("local_begin", 1), ("topk", 0), ("topk", 17),
-       ("num_tokens", 1 << 30), ("dtype", 4), ("dtype", -1), ("max_rows", -1), ("max_rows", 129), ("token_stride", 99),
+       ("num_tokens", 1 << 30), ("num_tokens", (1 << 30) - (1 << 16) + 1), ("dtype", 4), ("dtype", -1), ("max_rows", -1), ("max_rows", 129), ("token_stride", 99),
        ("token_stride", -100), ("row_stride", 1), ("row_stride", (1 << 40) + 1)]
 
 

@@ -290,6 +290,43 @@ def test_plain_product_without_offsets(rows, variant):
     assert torch.equal(p.run((a, asf, b, bsf, None)).double(), p.ref())
 
 
+@pytest.mark.parametrize("variant", [0, 1])
+def test_product_many_groups(variant):
+    """1024 groups, most of them empty: the tile plan's largest size."""
+    r = np.random.RandomState(3)
+    sizes = np.where(r.rand(1024) < 0.8, 0, r.randint(1, 12, 1024))
+    sizes[700] = 300
+    p = Product(list(sizes), 20, 160, seed=8, variant=variant)
+    assert torch.equal(p.run().double(), p.ref())
+
+
+@pytest.mark.parametrize("variant", [0, 1])
+def test_products_on_two_streams_at_once(variant):
+    ps = [Product([200, 0, 313], 300, 2048, seed=s, variant=variant) for s in (1, 2)]
+    args = [p.args() for p in ps]
+    out = [torch.zeros(p.rows, p.N, device="cuda") for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, a, c, s in zip(ps, args, out, streams):
+            B.moe_mxfp4_gemm(p.desc, *a, c, stream=s)
+    torch.cuda.synchronize()
+    for p, c in zip(ps, out):
+        assert torch.equal(c.cpu().double(), p.ref())
+
+
+@pytest.mark.parametrize("variant", [0, 1])
+def test_product_scales_on_a_4_byte_boundary(variant):
+    p = Product([90], 64, 256, seed=3, la="rows", lb="rows", variant=variant)
+    a, asf, b, bsf, off = p.args()
+    shifted = []
+    for s in (asf, bsf):
+        buf = torch.zeros(s.numel() + 4, dtype=torch.uint8, device="cuda")
+        buf[4:] = s.reshape(-1)
+        shifted.append(buf[4:])
+    assert torch.equal(p.run((a, shifted[0], b, shifted[1], off)).double(), p.ref())
+
+
 def test_product_offsets_past_32_bits():
     """Weights of more than 2^32 code bytes and results past 2^31 elements from the start."""
     G, N, K = 3, 1 << 17, 1 << 15  # 2^31 bytes of codes a group
