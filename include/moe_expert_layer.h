@@ -11,6 +11,10 @@
  *   FC2      down-projection grouped GEMM
  *   combine  top-k weighted sum back into token order (no atomics, fixed slot order)
  *
+ * Beside the layer (at the end of this file): its parts for callers with a router or experts of
+ * their own (tokens sorted by expert and back, with gradients), and MXFP4 quantisation and
+ * grouped products.
+ *
  * Sources: the fused "Mega MoE" expert layer as described by DeepGEMM PR #445
  * ("fix(sm90): support parameterized SwiGLU in FP8 MegaMoE": Summary, Changes,
  * Compatibility), DeepGEMM PR #386 ("... native UE8M0, and direct combine":

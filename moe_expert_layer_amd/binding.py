@@ -375,22 +375,22 @@ class _DispatchView:
             _rows_tensor(name, t, self.dtype, *self.rows, self.row_stride[0], dev, at_least=True)
 
 
-_views = {}  # descriptor bytes -> _DispatchView: a descriptor may change between calls, its bytes say whether it did
+_views = {}  # (view's class, descriptor bytes) -> view: a descriptor may change between calls, its bytes say whether it did
 
 
-def _view(desc) -> _DispatchView:
-    key = bytes(desc)
+def _view(cls, desc):
+    key = (cls, bytes(desc))
     v = _views.get(key)
     if v is None:
         if len(_views) >= 1024:
             _views.clear()
-        v = _views[key] = _DispatchView(desc)
+        v = _views[key] = cls(desc)
     return v
 
 
 def moe_sort_tokens(desc, topk_ids, counts, offsets, row_to_slot, slot_to_row, workspace, stream=None):
     """Expert ids int32 [T, k] -> counts, offsets, row_to_slot, slot_to_row (int32), as moe_route_permute writes them."""
-    v, dev = _view(desc), _device_of(topk_ids)
+    v, dev = _view(_DispatchView, desc), _device_of(topk_ids)
     n, i32 = v.slots, v.i32
     _array("topk_ids", topk_ids, i32, n, dev)
     _array("counts", counts, i32, v.num_local, dev)
@@ -404,7 +404,7 @@ def moe_sort_tokens(desc, topk_ids, counts, offsets, row_to_slot, slot_to_row, w
 
 def moe_dispatch(desc, x, slot_to_row, xs, stream=None):
     """Token rows x [T, H] -> expert-ordered rows xs [max_rows, H] (rows that no slot owns are left as they were)."""
-    v, dev = _view(desc), _device_of(x)
+    v, dev = _view(_DispatchView, desc), _device_of(x)
     v.token_tensor("x", x, dev)
     _array("slot_to_row", slot_to_row, v.i32, v.slots, dev)
     v.expert_tensor("xs", xs, dev)
@@ -413,7 +413,7 @@ def moe_dispatch(desc, x, slot_to_row, xs, stream=None):
 
 def moe_dispatch_backward(desc, dxs, slot_to_row, dx, stream=None):
     """Gradient of moe_dispatch: dx[t] = the sum of the rows of dxs that token t went to."""
-    v, dev = _view(desc), _device_of(dxs)
+    v, dev = _view(_DispatchView, desc), _device_of(dxs)
     v.expert_tensor("dxs", dxs, dev)
     _array("slot_to_row", slot_to_row, v.i32, v.slots, dev)
     v.token_tensor("dx", dx, dev)
@@ -423,7 +423,7 @@ def moe_dispatch_backward(desc, dxs, slot_to_row, dx, stream=None):
 
 def moe_combine(desc, ys, slot_to_row, topk_w, y, stream=None):
     """Expert-ordered rows ys -> y[t] = sum_j topk_w[t, j] * ys[slot_to_row[t, j]], in token order."""
-    v, dev = _view(desc), _device_of(ys)
+    v, dev = _view(_DispatchView, desc), _device_of(ys)
     v.expert_tensor("ys", ys, dev)
     _array("slot_to_row", slot_to_row, v.i32, v.slots, dev)
     _array("topk_w", topk_w, v.f32, v.slots, dev)
@@ -435,7 +435,7 @@ def moe_combine(desc, ys, slot_to_row, topk_w, y, stream=None):
 def moe_combine_backward(desc, dy, ys, slot_to_row, topk_w, dys, dw, topk_ids=None, dlogits=None, stream=None):
     """Gradients of moe_combine: dys (rows), dw [T, k] float32 and, where dlogits [T, E_tot] float32 is given
     (with topk_ids), the gradient of the routing logits under the softmax over the chosen ones."""
-    v, dev = _view(desc), _device_of(dy)
+    v, dev = _view(_DispatchView, desc), _device_of(dy)
     v.token_tensor("dy", dy, dev)
     v.expert_tensor("ys", ys, dev)
     _array("slot_to_row", slot_to_row, v.i32, v.slots, dev)
@@ -465,20 +465,39 @@ def make_mxfp4_gemm_desc(rows: int, n: int, k: int, groups: int = 1, out_dtype: 
                             SCALE_LAYOUTS[b_scale_layout], variant, out_stride)
 
 
-def _codes_and_scales(name, codes, sf, rows, k, layout, dev):
-    T = _torch()
-    _array(name, codes, T.u8, rows * (k // 2), dev)
-    if layout == MOE_SF_PACKED_MN:
-        _array(name + "_sf", sf, T.i32, (k // 32 + 3) // 4 * ((rows + 3) // 4 * 4), dev)
-    else:
-        _array(name + "_sf", sf, T.u8, rows * (k // 32), dev)
+class _Stored:
+    """How many codes and scales rows of k MXFP4 values have, and in which type."""
+
+    def __init__(self, rows, k, layout):
+        packed = layout == MOE_SF_PACKED_MN
+        self.n, self.u8 = rows * (k // 2), _torch().u8
+        self.sf_type = _torch().i32 if packed else self.u8
+        self.sf_n = (k // 32 + 3) // 4 * ((rows + 3) // 4 * 4) if packed else rows * (k // 32)
+
+    def check(self, name, codes, sf, dev):
+        _array(name, codes, self.u8, self.n, dev)
+        _array(name + "_sf", sf, self.sf_type, self.sf_n, dev)
+
+
+class _Mxfp4View:
+    def __init__(self, d):
+        self.stored, self.dtype = _Stored(d.rows, d.k, d.scale_layout), _torch_dtype(d.dtype)
+        self.rows, self.k, self.stride = d.rows, d.k, d.stride or d.k
+
+
+class _Mxfp4GemmView:
+    def __init__(self, d):
+        self.a = _Stored(d.rows, d.k, d.a_scale_layout)
+        self.b = _Stored(d.groups * d.n, d.k, d.b_scale_layout)
+        self.i32, self.offsets = _torch().i32, d.groups + 1
+        self.dtype, self.rows, self.n, self.stride = _torch_dtype(d.out_dtype), d.rows, d.n, d.out_stride or d.n
 
 
 def moe_quantize_mxfp4(desc, values, codes, sf, stream=None):
     """values [rows, k] -> E2M1 codes uint8 [rows, k / 2] and UE8M0 scales (uint8, or int32 words when packed)."""
-    dev = _device_of(values)
-    _rows_tensor("values", values, _torch_dtype(desc.dtype), desc.rows, desc.k, desc.stride or desc.k, dev)
-    _codes_and_scales("codes", codes, sf, desc.rows, desc.k, desc.scale_layout, dev)
+    v, dev = _view(_Mxfp4View, desc), _device_of(values)
+    _rows_tensor("values", values, v.dtype, v.rows, v.k, v.stride, dev)
+    v.stored.check("codes", codes, sf, dev)
     _launch(lib().moe_quantize_mxfp4, dev, stream, ctypes.byref(desc), values.data_ptr(), codes.data_ptr(), sf.data_ptr())
 
 
@@ -486,9 +505,9 @@ def moe_dequantize_mxfp4(desc, codes, sf, values, dtype: Optional[str] = None, s
     """The values [rows, k] of codes and scales, in the descriptor's dtype (or the one named)."""
     if dtype is not None and DTYPES[dtype] != desc.dtype:
         desc = MoeMxfp4Desc(desc.rows, desc.k, DTYPES[dtype], desc.scale_layout, desc.stride)
-    dev = _device_of(codes)
-    _codes_and_scales("codes", codes, sf, desc.rows, desc.k, desc.scale_layout, dev)
-    _rows_tensor("values", values, _torch_dtype(desc.dtype), desc.rows, desc.k, desc.stride or desc.k, dev)
+    v, dev = _view(_Mxfp4View, desc), _device_of(codes)
+    v.stored.check("codes", codes, sf, dev)
+    _rows_tensor("values", values, v.dtype, v.rows, v.k, v.stride, dev)
     _launch(lib().moe_dequantize_mxfp4, dev, stream, ctypes.byref(desc), codes.data_ptr(), sf.data_ptr(),
             values.data_ptr())
 
@@ -496,12 +515,11 @@ def moe_dequantize_mxfp4(desc, codes, sf, values, dtype: Optional[str] = None, s
 def moe_mxfp4_gemm(desc, a, a_sf, b, b_sf, offsets, c, stream=None):
     """c[r] = a[r] @ b[e].T for the rows of each group e (offsets int32 [groups + 1]; None: one group of all rows);
     a, b: E2M1 codes with their scales, c [rows, n].  Rows past the last group are left as they were."""
-    T = _torch()
-    dev = _device_of(a)
-    _codes_and_scales("a", a, a_sf, desc.rows, desc.k, desc.a_scale_layout, dev)
-    _codes_and_scales("b", b, b_sf, desc.groups * desc.n, desc.k, desc.b_scale_layout, dev)
+    v, dev = _view(_Mxfp4GemmView, desc), _device_of(a)
+    v.a.check("a", a, a_sf, dev)
+    v.b.check("b", b, b_sf, dev)
     if offsets is not None:
-        _array("offsets", offsets, T.i32, desc.groups + 1, dev)
-    _rows_tensor("c", c, _torch_dtype(desc.out_dtype), desc.rows, desc.n, desc.out_stride or desc.n, dev)
+        _array("offsets", offsets, v.i32, v.offsets, dev)
+    _rows_tensor("c", c, v.dtype, v.rows, v.n, v.stride, dev)
     _launch(lib().moe_mxfp4_gemm, dev, stream, ctypes.byref(desc), a.data_ptr(), a_sf.data_ptr(), b.data_ptr(),
             b_sf.data_ptr(), _ptr(offsets), c.data_ptr())
