@@ -9,11 +9,16 @@ namespace moe {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopk = 16;
 constexpr int kMaxShared = 4;  // shared experts per layer
-constexpr int kPermChunk = 1024;  // slots per permute workgroup (a multiple of 256, at most 4096)
-constexpr int kPermTinySlots = 8192;    // at most this many slots and ...
+// The permute's kernels (ids -> maps, from Python, k = 8): one workgroup without atomics (4096 slots and 63 local
+// experts: 7.0 us, 8192: 11), one with them (512 slots and 256 local experts: 6.6 us, 2048: 8.8, 8192: 19), or
+// chunks over many workgroups in two launches (8.7 us up to 32768 slots) or three (11.4 us, but 11.8 instead of 13.4
+// from 131072 slots and 256 local experts, 21 instead of 39 from 524288).
+constexpr int kPermChunk = 1024;  // slots per permute workgroup
+constexpr int kPermTinySlots = 6144;    // at most this many slots and ...
 constexpr int kPermTinyBuckets = 64;    // ... 63 local experts: the one-workgroup permute without atomics
-constexpr int kPermSmallSlots = 16384;  // at most this many slots: one-workgroup permute
+constexpr int kPermSmallSlots = 2048;   // at most this many slots: one-workgroup permute
 constexpr int kPermSmallBuckets = 257;  // ... and at most 256 local experts
+constexpr int kPermSelfLoads = 64;      // at most this many chunk counts per thread: no launch of its own to add them
 
 struct Shape {
   int T, H, I, E, e0, EL, k;

@@ -221,99 +221,32 @@ __global__ __launch_bounds__(256) void permute_hist_kernel(const int32_t* __rest
   for (int b = threadIdx.x; b < NB; b += 256) chunk_cnt[(size_t)blockIdx.x * NB + b] = hist[b];
 }
 
-// One workgroup: per-bucket running sums over chunks, then an exclusive scan over buckets.
+// A wave per bucket: its chunk counts become exclusive prefixes over the chunks, 256 chunks per pass.  The
+// 16 waves of a workgroup take buckets side by side, so that they share the lines of chunk_cnt [chunk][bucket].
 __global__ __launch_bounds__(1024) void permute_scan_kernel(const int32_t* __restrict__ chunk_cnt, int nchunks, int EL,
-                                                            int bm, int32_t* __restrict__ chunk_base,
-                                                            int32_t* __restrict__ counts,
-                                                            int32_t* __restrict__ offsets,
-                                                            int32_t* __restrict__ plan) {
-  __shared__ int tot[2 * 1024 + 2];
-  __shared__ int mt[2 * 1024 + 2];
+                                                            int32_t* __restrict__ chunk_base,
+                                                            int32_t* __restrict__ counts) {
   const int NB = EL + 1;
-  for (int b = threadIdx.x; b < 2 * 1024; b += blockDim.x) tot[b] = mt[b] = 0;
-  __syncthreads();
-  // one wave per bucket: its chunk counts, 64 chunks per pass, become exclusive prefixes
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int b = wave; b < NB; b += 16) {
-    int carry = 0;
-    for (int c0 = 0; c0 < nchunks; c0 += 64) {  // uniform
-      const int c = c0 + lane;
-      const size_t at = (size_t)c * NB + b;
-      const int v = c < nchunks ? chunk_cnt[at] : 0;
-      const int inc = wave_inclusive_scan_dpp(v);
-      if (c < nchunks) chunk_base[at] = carry + inc - v;
+  const int b = blockIdx.x * 16 + wave;
+  if (b >= NB) return;
+  int carry = 0;
+  for (int c0 = 0; c0 < nchunks; c0 += 256) {
+    int v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + i * 64 + lane;
+      v[i] = c < nchunks ? chunk_cnt[(size_t)c * NB + b] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + i * 64 + lane;
+      const int inc = wave_inclusive_scan_dpp(v[i]);
+      if (c < nchunks) chunk_base[(size_t)c * NB + b] = carry + inc - v[i];
       carry += __builtin_amdgcn_readlane(inc, 63);
     }
-    if (lane == 0) {
-      tot[b] = carry;
-      if (b < EL) mt[b] = (carry + bm - 1) / bm;  // m-tiles of this expert
-    }
   }
-  __syncthreads();
-  block_exclusive_scan_2048(tot);  // tot[b] <- sum of tot[0..b)
-  block_exclusive_scan_2048(mt);
-  for (int b = threadIdx.x; b < NB; b += blockDim.x) {
-    offsets[b] = tot[b];
-    plan[b] = mt[b];
-    if (b < EL) counts[b] = tot[b + 1] - tot[b];
-  }
-}
-
-// Stable scatter: slots in ascending order within each bucket.
-__global__ __launch_bounds__(256) void permute_scatter_kernel(const int32_t* __restrict__ ids, int nslots, int e0,
-                                                              int EL, const int32_t* __restrict__ chunk_base,
-                                                              const int32_t* __restrict__ offsets,
-                                                              int32_t* __restrict__ row_to_slot,
-                                                              int32_t* __restrict__ slot_to_row) {
-  extern __shared__ int sm[];
-  const int NB = EL + 1;
-  int* base = sm;       // [NB]
-  int* wcnt = sm + NB;  // [4][NB]
-  for (int b = threadIdx.x; b < NB; b += 256) {
-    base[b] = offsets[b] + chunk_base[(size_t)blockIdx.x * NB + b];
-    wcnt[b] = wcnt[NB + b] = wcnt[2 * NB + b] = wcnt[3 * NB + b] = 0;
-  }
-  __syncthreads();
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  int nbits = 1;
-  while ((1 << nbits) < NB) ++nbits;
-  const uint64_t lt = (lane == 0) ? 0ull : ((~0ull) >> (64 - lane));
-  for (int r = 0; r < kPermChunk / 256; ++r) {
-    const int s = blockIdx.x * kPermChunk + r * 256 + threadIdx.x;
-    const bool valid = s < nslots;
-    const int b = valid ? bucket_of(ids[s], e0, EL) : 0;
-    uint64_t match = __ballot(valid);
-    for (int bit = 0; bit < nbits; ++bit) {
-      const bool on = (b >> bit) & 1;
-      const uint64_t m = __ballot(valid && on);
-      match &= on ? m : ~m;
-    }
-    const int rank = __popcll(match & lt);
-    const int cnt = __popcll(match);
-    const bool leader = valid && rank == 0;
-    if (leader) wcnt[wave * NB + b] = cnt;
-    __syncthreads();
-    int pos = 0;
-    if (valid) {
-      pos = base[b] + rank;
-      for (int q = 0; q < wave; ++q) pos += wcnt[q * NB + b];
-    }
-    __syncthreads();
-    if (leader) {
-      atomicAdd(&base[b], cnt);
-      wcnt[wave * NB + b] = 0;
-    }
-    __syncthreads();
-    if (valid) {
-      if (b < EL) {
-        row_to_slot[pos] = s;
-        slot_to_row[s] = pos;
-      } else {
-        row_to_slot[pos] = -1;
-        slot_to_row[s] = -1;
-      }
-    }
-  }
+  if (lane == 0 && b < EL) counts[b] = carry;
 }
 
 // Everything in one workgroup when the slots are few (decode-sized calls): histogram,
@@ -416,7 +349,7 @@ __global__ __launch_bounds__(1024) void permute_small_kernel(const int32_t* __re
   }
 }
 
-// One workgroup, no atomics (up to 8192 slots, up to 63 local experts): the slots form
+// One workgroup, no atomics (up to kPermTinySlots slots, up to 63 local experts): the slots form
 // chunks of 64 in slot order (round r of wave w is chunk 16 r + w).  Each wave ranks its
 // slots among the equal buckets of its chunk with ballots and one lane per bucket stores
 // the chunk's count; a wave per bucket turns the counts into exclusive prefixes over the
@@ -500,35 +433,108 @@ __global__ __launch_bounds__(1024) void permute_tiny_kernel(const int32_t* __res
   }
 }
 
-// Stable scatter of one chunk (kPermChunk slots) for up to 63 local experts, without
-// per-round barriers: every wave ranks its slots of all kPermChunk / 256 rounds by ballot
-// matching (sub-chunk 4 r + w holds the chunk's slots [256 r + 64 w, + 64), so sub-chunks are
-// in slot order),
-// one wave per bucket turns the sub-chunk counts into exclusive prefixes, and each slot's
-// position is offset + the chunk's base + the prefix of its sub-chunk + its rank.
-__global__ __launch_bounds__(256) void permute_scatter64_kernel(const int32_t* __restrict__ ids, int nslots, int e0,
-                                                                int EL, const int32_t* __restrict__ chunk_base,
-                                                                const int32_t* __restrict__ offsets,
-                                                                int32_t* __restrict__ row_to_slot,
-                                                                int32_t* __restrict__ slot_to_row) {
-  constexpr int kRounds = kPermChunk / 256;
-  constexpr int kSub = kRounds * 4;  // sub-chunks of 64 slots (one per wave and round)
-  static_assert(kSub <= 64 && kPermChunk % 256 == 0, "one lane per sub-chunk in the prefix");
-  __shared__ int sc[kPermTinyBuckets][kSub];  // [bucket][sub-chunk]: count, then prefix
-  __shared__ int base[kPermTinyBuckets];
+// This thread's exclusive prefix of x over the 512 threads of a workgroup; all: their sum.  wsum: 8 ints of
+// LDS, free again after the next barrier.
+__device__ __forceinline__ int scan_512(int x, int* wsum, int& all) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int inc = wave_inclusive_scan_dpp(x);
+  if (lane == 63) wsum[wave] = inc;
+  __syncthreads();
+  int before = 0;
+  all = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int v = wsum[q];
+    all += v;
+    before += q < wave ? v : 0;
+  }
+  return before + inc - x;
+}
+
+// Stable scatter of one chunk (kPermChunk slots): every wave ranks its slots of both rounds by ballot
+// matching (sub-chunk 8 r + w holds the chunk's slots [512 r + 64 w, + 64), so sub-chunks are in slot
+// order), one thread per bucket turns the sub-chunk counts into exclusive prefixes, and each slot's
+// position is the bucket's offset + the prefix of the chunk + that of its sub-chunk + its rank.
+// SELF: no scan kernel ran; every workgroup adds up the chunks' counts itself, with the chunks dealt to
+// 512 / lanes groups of threads (lanes: the least power of two that is at least the buckets; at most 512).
+// The first workgroup writes the offsets, the tile plan and, for SELF, the counts (else they are inputs).
+// 32768 slots, 32 of 256 experts: latency (ids, counts, ranks, stores in turn); the whole permute takes 7.9 us in
+// two launches and 11.4 us with a scan kernel between them.
+template <bool SELF>
+__global__ __launch_bounds__(512) void permute_scatter_kernel(const int32_t* __restrict__ ids, int nslots, int e0,
+                                                              int EL, const int32_t* __restrict__ chunk_cnt,
+                                                              const int32_t* __restrict__ chunk_base, int lanes_log2,
+                                                              int bm, int32_t* __restrict__ counts,
+                                                              int32_t* __restrict__ offsets,
+                                                              int32_t* __restrict__ plan,
+                                                              int32_t* __restrict__ row_to_slot,
+                                                              int32_t* __restrict__ slot_to_row) {
+  constexpr int kRounds = kPermChunk / 512, kSub = kRounds * 8;
+  static_assert(kSub == 16, "two 16-byte words of sub-chunk counts per bucket");
+  extern __shared__ uint4 sub[];  // [NB][2]: uint16 counts of the 16 sub-chunks, then their prefixes
+  __shared__ int base[kMaxExperts + 1];
+  __shared__ int part[SELF ? 2 : 1][512];  // SELF: each group's sums over all chunks and over those before this one
+  __shared__ int wsum[2][8];
+  uint16_t* sc = reinterpret_cast<uint16_t*>(sub);
   const int NB = EL + 1;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int first = blockIdx.x * kPermChunk;
-  for (int i = tid; i < kPermTinyBuckets * kSub; i += 256) (&sc[0][0])[i] = 0;
-  for (int b = tid; b < NB; b += 256) base[b] = offsets[b] + chunk_base[(size_t)blockIdx.x * NB + b];
   int bk[kRounds];
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
-    const int s = first + r * 256 + tid;
+    const int s = first + r * 512 + tid;
     const int id = load_clamped(ids, s, nslots);
     bk[r] = s < nslots ? bucket_of(id, e0, EL) : -1;
   }
+  int v0 = 0, v1 = 0;  // slots of experts 2 tid and 2 tid + 1
+  if (SELF) {
+    const int lanes = 1 << lanes_log2, b = tid & (lanes - 1), step = 512 >> lanes_log2;
+    int all = 0, before = 0;
+#pragma unroll 8
+    for (int c = tid >> lanes_log2; c < (int)gridDim.x; c += step) {
+      const int v = chunk_cnt[c * NB + (b < NB ? b : 0)];
+      all += v;
+      before += c < (int)blockIdx.x ? v : 0;
+    }
+    part[0][tid] = all;
+    part[1][tid] = before;
+  } else {
+    if (2 * tid < EL) v0 = counts[2 * tid];
+    if (2 * tid + 1 < EL) v1 = counts[2 * tid + 1];
+  }
+  for (int i = tid; i < 2 * NB; i += 512) sub[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
+  if (SELF) {
+    const int lanes = 1 << lanes_log2;
+    for (int g = 0; g < 512; g += lanes) {
+      if (2 * tid < EL) v0 += part[0][g + 2 * tid];
+      if (2 * tid + 1 < EL) v1 += part[0][g + 2 * tid + 1];
+    }
+  }
+  int local;
+  const int off = scan_512(v0 + v1, wsum[0], local);
+  if (2 * tid < EL) base[2 * tid] = off;
+  if (2 * tid + 1 < EL) base[2 * tid + 1] = off + v0;
+  if (tid == 0) base[EL] = local;
+  if (blockIdx.x == 0) {
+    const int m0 = (v0 + bm - 1) / bm, m1 = (v1 + bm - 1) / bm;  // m-tiles of the two experts
+    int tiles;
+    const int at = scan_512(m0 + m1, wsum[1], tiles);
+    if (2 * tid < EL) {
+      offsets[2 * tid] = off;
+      plan[2 * tid] = at;
+      if (SELF) counts[2 * tid] = v0;
+    }
+    if (2 * tid + 1 < EL) {
+      offsets[2 * tid + 1] = off + v0;
+      plan[2 * tid + 1] = at + m0;
+      if (SELF) counts[2 * tid + 1] = v1;
+    }
+    if (tid == 0) {
+      offsets[EL] = local;
+      plan[EL] = tiles;
+    }
+  }
   int nbits = 1;
   while ((1 << nbits) < NB) ++nbits;
   const uint64_t lt = (lane == 0) ? 0ull : ((~0ull) >> (64 - lane));
@@ -544,21 +550,36 @@ __global__ __launch_bounds__(256) void permute_scatter64_kernel(const int32_t* _
       match &= on ? m : ~m;
     }
     rank[r] = __popcll(match & lt);
-    if (valid && rank[r] == 0) sc[b][r * 4 + wave] = __popcll(match);
+    if (valid && rank[r] == 0) sc[b * kSub + r * 8 + wave] = (uint16_t)__popcll(match);
   }
   __syncthreads();
-  for (int b = wave; b < NB; b += 4) {
-    const int v = lane < kSub ? sc[b][lane] : 0;
-    const int ex = wave_inclusive_scan_dpp(v) - v;
-    if (lane < kSub) sc[b][lane] = ex;
+  for (int b = tid; b < NB; b += 512) {
+    uint32_t w[kSub / 2];
+    *reinterpret_cast<uint4*>(w) = sub[2 * b];
+    *reinterpret_cast<uint4*>(w + 4) = sub[2 * b + 1];
+    uint32_t run = 0;  // at most kPermChunk
+#pragma unroll
+    for (int i = 0; i < kSub / 2; ++i) {
+      const uint32_t lo = w[i] & 0xffffu, hi = w[i] >> 16;
+      w[i] = run | ((run + lo) << 16);
+      run += lo + hi;
+    }
+    sub[2 * b] = *reinterpret_cast<uint4*>(w);
+    sub[2 * b + 1] = *reinterpret_cast<uint4*>(w + 4);
+    int before = 0;
+    if (SELF)
+      for (int g = 0; g < 512; g += 1 << lanes_log2) before += part[1][g + b];
+    else
+      before = chunk_base[(size_t)blockIdx.x * NB + b];
+    base[b] += before;
   }
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
     const int b = bk[r];
     if (b < 0) continue;
-    const int s = first + r * 256 + tid;
-    const int pos = base[b] + sc[b][r * 4 + wave] + rank[r];
+    const int s = first + r * 512 + tid;
+    const int pos = base[b] + sc[b * kSub + r * 8 + wave] + rank[r];
     row_to_slot[pos] = b < EL ? s : -1;
     slot_to_row[s] = b < EL ? pos : -1;
   }
@@ -576,22 +597,23 @@ hipError_t launch_permute(const int32_t* ids, int nslots, int e0, int EL, int32_
     permute_small_kernel<<<1, 1024, 0, s>>>(ids, nslots, e0, EL, bm, counts, offsets, row_to_slot, slot_to_row, plan);
     return hipGetLastError();
   }
-  const int nchunks = (nslots + kPermChunk - 1) / kPermChunk;
-  if (nchunks > 0) {
-    permute_hist_kernel<<<nchunks, 256, NB * sizeof(int), s>>>(ids, nslots, e0, EL, chunk_cnt);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  permute_scan_kernel<<<1, 1024, 0, s>>>(chunk_cnt, nchunks, EL, bm, chunk_base, counts, offsets, plan);
+  const int nchunks = (nslots + kPermChunk - 1) / kPermChunk;  // nslots is not 0 here
+  permute_hist_kernel<<<nchunks, 256, NB * sizeof(int), s>>>(ids, nslots, e0, EL, chunk_cnt);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || nchunks == 0) return e;
-  if (NB <= kPermTinyBuckets) {
-    permute_scatter64_kernel<<<nchunks, 256, 0, s>>>(ids, nslots, e0, EL, chunk_base, offsets, row_to_slot,
-                                                      slot_to_row);
+  if (e != hipSuccess) return e;
+  int lanes_log2 = 6;
+  while ((1 << lanes_log2) < NB) ++lanes_log2;
+  const size_t lds = (size_t)NB * 2 * sizeof(uint4);
+  if (lanes_log2 <= 9 && (nchunks << lanes_log2) <= kPermSelfLoads * 512) {
+    permute_scatter_kernel<true><<<nchunks, 512, lds, s>>>(ids, nslots, e0, EL, chunk_cnt, nullptr, lanes_log2, bm,
+                                                           counts, offsets, plan, row_to_slot, slot_to_row);
     return hipGetLastError();
   }
-  permute_scatter_kernel<<<nchunks, 256, 5 * NB * sizeof(int), s>>>(ids, nslots, e0, EL, chunk_base, offsets,
-                                                                     row_to_slot, slot_to_row);
+  permute_scan_kernel<<<(NB + 15) / 16, 1024, 0, s>>>(chunk_cnt, nchunks, EL, chunk_base, counts);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  permute_scatter_kernel<false><<<nchunks, 512, lds, s>>>(ids, nslots, e0, EL, nullptr, chunk_base, lanes_log2, bm,
+                                                          counts, offsets, plan, row_to_slot, slot_to_row);
   return hipGetLastError();
 }
 

@@ -58,6 +58,21 @@ def test_sort(T, E, e0, el, k, dup):
         assert np.array_equal(got.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("T,E,e0,el,k", [
+    (6144, 70, 3, 63, 1), (6145, 70, 3, 63, 1), (6145, 70, 3, 64, 1), (2048, 300, 9, 256, 1), (2049, 300, 9, 256, 1),
+    (2048, 300, 9, 257, 1), (8192, 16, 0, 16, 8), (32768, 300, 0, 127, 2), (32769, 300, 0, 128, 2),
+    (65536, 512, 0, 511, 1), (65537, 512, 0, 511, 1), (65536, 512, 0, 512, 1), (30000, 1024, 0, 1024, 3),
+    (200000, 300, 100, 100, 4), (1 << 20, 8, 7, 1, 1)])
+def test_sort_at_the_boundaries_of_its_kernels(T, E, e0, el, k):
+    g = torch.Generator().manual_seed(T + el)
+    p = torch.rand(E, generator=g) ** 4  # uneven: some experts have most of the slots, some none
+    p[torch.randperm(E, generator=g)[:E // 4]] = 0
+    ids = torch.multinomial(p, T * k, replacement=True, generator=g).to(torch.int32).view(T, k)
+    d = B.make_dispatch_desc(T, 8, E, k, local_begin=e0, num_local=el)
+    for got, want in zip(run_sort(d, ids), sort_ref(ids, e0, el)):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_sort_ids_outside_every_expert():
     ids = torch.tensor([[0, -1], [2147483647, 3], [-2147483648, 1], [7, 8]], dtype=torch.int32)
     d = B.make_dispatch_desc(4, 8, 8, 2, local_begin=1, num_local=7)
