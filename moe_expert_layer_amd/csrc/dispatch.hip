@@ -12,9 +12,10 @@
 // writer, so results do not depend on scheduling.
 //
 // All four move rows and do next to no arithmetic: what bounds them is HBM (large calls) or the
-// latency of one chain map -> row -> store (small ones).  A workgroup takes one token at a time: the
-// first k lanes of every wave load its map entries in one instruction, a ballot compacts the slots
-// that have a row, and the row loads are issued before any of them is used.
+// latency of one chain map -> row -> store (small ones).  A workgroup takes one token at a time, or,
+// where rows are short, each wave or pair of waves one of its own: the first k lanes of every wave load
+// its map entries in one instruction, a ballot compacts the slots that have a row, and the row loads are
+// issued before any of them is used.
 #include <hip/hip_runtime.h>
 #include <cstdint>
 
@@ -24,44 +25,47 @@
 
 namespace moe {
 
-// The rows of token t's slots, in lane j's register for slot j < k (any wave); the mask has bit j
+// The rows of the first n slots of token t, in lane j's register for slot j (any wave); the mask has bit j
 // set when slot j has a row below max_rows (a map entry outside [0, max_rows) counts as none).
-__device__ __forceinline__ uint64_t token_rows(const int32_t* __restrict__ s2r, long long t, int k, int max_rows,
+__device__ __forceinline__ uint64_t token_rows(const int32_t* __restrict__ s2r, long long t, int k, int n, int max_rows,
                                                int lane, int& row) {
-  row = lane < k ? s2r[t * k + lane] : -1;
+  row = lane < n ? s2r[t * k + lane] : -1;
   return __ballot((unsigned)row < (unsigned)max_rows);
 }
 
-// grid (column chunks, tokens): 256 threads, kDispatchPer 16-byte chunks of the token's row each, read once
+// grid (column chunks, tokens): 256 threads on 1, 2 or 4 tokens, kDispatchPer 16-byte chunks of a row each, read once
 // and stored to every row the token has (a kernel by rows would read a token up to k times).  128 tokens of
 // 14 KB, 128 rows: 3.4 us, the latency of map -> row -> store.
 constexpr int kDispatchPer = 2;
 
 __global__ __launch_bounds__(256) void dispatch_kernel(const uint8_t* __restrict__ x, long long x_pitch,
                                                        const int32_t* __restrict__ s2r, int T, int k, int max_rows,
-                                                       long long row_bytes, uint8_t* __restrict__ xs,
+                                                       int waves_log2, long long row_bytes, uint8_t* __restrict__ xs,
                                                        long long xs_pitch) {
-  const int lane = threadIdx.x & 63;
-  const long long c0 = ((long long)blockIdx.x * (256 * kDispatchPer) + threadIdx.x) * 16;
+  const int lane = threadIdx.x & 63, lanes = 64 << waves_log2, pitch = lanes * 16;
+  const long long c0 = ((long long)blockIdx.x * (lanes * kDispatchPer) + (threadIdx.x & (lanes - 1))) * 16;
   // the row's last, partial chunk, where it is one of this lane's
-  const long long whole = row_bytes & ~15LL, last = whole == c0 || whole == c0 + 4096 ? whole : row_bytes;
+  const long long whole = row_bytes & ~15LL, last = whole == c0 || whole == c0 + pitch ? whole : row_bytes;
   static_assert(kDispatchPer == 2, "");
-  for (int t = blockIdx.y; t < T; t += gridDim.y) {
+  const int tg = __builtin_amdgcn_readfirstlane(threadIdx.x >> (6 + waves_log2)), tokens = 4 >> waves_log2;
+  for (int t0 = blockIdx.y * tokens; t0 < T; t0 += gridDim.y * tokens) {
+    const int t = t0 + tg;
     int row;
-    uint64_t mask = token_rows(s2r, t, k, max_rows, lane, row);
+    if (t >= T) break;
+    uint64_t mask = token_rows(s2r, t, k, k, max_rows, lane, row);
     if (mask == 0) continue;
     const uint8_t* src = x + (long long)t * x_pitch;
     u32x4 v[kDispatchPer];
 #pragma unroll
     for (int i = 0; i < kDispatchPer; ++i)
-      if (c0 + i * 4096 + 16 <= row_bytes) v[i] = load16(src + c0 + i * 4096);
+      if (c0 + i * pitch + 16 <= row_bytes) v[i] = load16(src + c0 + i * pitch);
     while (mask) {
       const int j = __builtin_ctzll(mask);
       mask &= mask - 1;
       uint8_t* dst = xs + (long long)__builtin_amdgcn_readlane(row, j) * xs_pitch;
 #pragma unroll
       for (int i = 0; i < kDispatchPer; ++i)
-        if (c0 + i * 4096 + 16 <= row_bytes) store16(dst + c0 + i * 4096, v[i]);
+        if (c0 + i * pitch + 16 <= row_bytes) store16(dst + c0 + i * pitch, v[i]);
       if (last < row_bytes)
         for (long long b = last; b < row_bytes; ++b) dst[b] = src[b];
     }
@@ -69,7 +73,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const uint8_t* __restrict
 }
 
 // y[t] = sum over the token's rows of weight * row (WEIGHTED) or of the rows themselves.
-// grid (column chunks, tokens): 256 threads, one 16-byte chunk each; the rows are taken four at a
+// grid (column chunks, tokens): 256 threads on 1, 2 or 4 tokens, one 16-byte chunk each; the rows are taken four at a
 // time, their loads issued before the sum.  32768 tokens of 7168 bfloat16 values with 32700 rows:
 // 193 us, 4.9 TB/s, what a copy of 2 GiB reaches; 4097 tokens of 2050 float32 values, 4 rows each:
 // 34 us, 4.9 TB/s; one token: 3.0 us.
@@ -77,14 +81,18 @@ template <typename T, bool WEIGHTED>
 __global__ __launch_bounds__(256) void combine_rows_kernel(const T* __restrict__ ys, long long ys_stride,
                                                            const int32_t* __restrict__ s2r,
                                                            const float* __restrict__ w, int ntok, int k, int max_rows,
-                                                           int H, T* __restrict__ y, long long y_stride) {
+                                                           int waves_log2, int H, T* __restrict__ y,
+                                                           long long y_stride) {
   constexpr int V = Elem<T>::kVec;
-  const int lane = threadIdx.x & 63;
-  const int c = (blockIdx.x * 256 + threadIdx.x) * V;
+  const int lane = threadIdx.x & 63, lanes = 64 << waves_log2;
+  const int c = (blockIdx.x * lanes + (threadIdx.x & (lanes - 1))) * V;
   const bool whole = c + V <= H;
-  for (int t = blockIdx.y; t < ntok; t += gridDim.y) {
+  const int tg = __builtin_amdgcn_readfirstlane(threadIdx.x >> (6 + waves_log2)), tokens = 4 >> waves_log2;
+  for (int t0 = blockIdx.y * tokens; t0 < ntok; t0 += gridDim.y * tokens) {
+    const int t = t0 + tg;
+    if (t >= ntok) break;
     int row;
-    uint64_t mask = token_rows(s2r, t, k, max_rows, lane, row);
+    uint64_t mask = token_rows(s2r, t, k, k, max_rows, lane, row);
     const float wl = WEIGHTED && lane < k ? w[(long long)t * k + lane] : 1.f;
     float acc[V];
 #pragma unroll
@@ -142,30 +150,33 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// One workgroup (NW waves) per token.  With n rows the waves split into n groups of P = NW / n: each
-// group takes one row, each of its waves every P-th 64-chunk piece of it, so the work is spread
-// whether a token has one local row or all k of them.  (n > NW: the waves take the rows in turn.)  dy is
-// read by every group, from the L1 after the first.  16384 tokens of 4096 bfloat16 values, 8 rows each:
+// G groups of NW waves in a workgroup, each with a token of its own.  With n rows the waves of a group
+// split into n parts of P = NW / n: each part takes one row, each of its waves every P-th 64-chunk piece
+// of it, so the work is spread whether a token has one local row or all k of them.  (n > NW: the waves
+// take the rows in turn.)  dy is read by every part, from the L1 after the first.  16384 tokens of 4096 bfloat16 values, 8 rows each:
 // 461 us, 5.0 TB/s, what a copy reaches; 512 tokens of 2048 float16 values, 4 rows each: 6.6 us.
-template <typename T, int NW>
-__global__ __launch_bounds__(NW * 64) void combine_backward_kernel(
+template <typename T, int NW, int G>
+__global__ __launch_bounds__(NW * G * 64) void combine_backward_kernel(
     const T* __restrict__ dy, long long dy_stride, const T* __restrict__ ys, long long row_stride,
     const int32_t* __restrict__ s2r, const float* __restrict__ w, int ntok, int k, int max_rows, int H,
     T* __restrict__ dys, float* __restrict__ dw, const int32_t* __restrict__ ids, int E, float* __restrict__ dlogits) {
   constexpr int V = Elem<T>::kVec, U = 4;  // chunks in flight per lane
-  __shared__ float part[16][NW];  // [slot][wave of its group]
-  __shared__ float g[16];
-  __shared__ int gid[16];
+  __shared__ float part[NW > 1 ? G : 1][16][NW];  // [token][slot][wave of its part]
+  __shared__ float gs[NW > 1 ? G : 1][16];
+  __shared__ int gids[NW > 1 ? G : 1][16];
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tg = wid / NW, wave = wid % NW;
   const int nchunk = H / V;  // whole 16-byte chunks of a row
-  for (int t = blockIdx.x; t < ntok; t += gridDim.x) {
+  for (int t0 = blockIdx.x * G; t0 < ntok; t0 += gridDim.x * G) {
+    const int t = t0 + tg;
+    const bool live = t < ntok;
     int row;
-    const uint64_t mask = token_rows(s2r, t, k, max_rows, lane, row);
-    const float wl = lane < k ? w[(long long)t * k + lane] : 0.f;
+    const uint64_t mask = token_rows(s2r, live ? t : 0, k, live ? k : 0, max_rows, lane, row);
+    const float wl = live && lane < k ? w[(long long)t * k + lane] : 0.f;
     const int n = __popcll(mask);
     const int P = n == 0 ? 1 : n < NW ? NW / n : 1;
     const T* dyt = dy + (long long)t * dy_stride;
+    float d = 0.f;  // lane j: the dot product of slot j
     for (int q = wave / P; q < n; q += NW / P) {  // q-th slot with a row; one pass unless n > NW
       uint64_t m = mask;
       for (int i = 0; i < q; ++i) m &= m - 1;
@@ -210,13 +221,17 @@ __global__ __launch_bounds__(NW * 64) void combine_backward_kernel(
         }
       }
       dot = wave_sum(dot);
-      if (lane == 0) part[j][p] = dot;
+      if (NW == 1)
+        d = lane == j ? dot : d;
+      else if (lane == 0)
+        part[tg][j][p] = dot;
     }
-    __syncthreads();
-    if (wave == 0) {
-      float d = 0.f;
-      if (lane < k && ((mask >> lane) & 1))
-        for (int p = 0; p < P; ++p) d += part[lane][p];
+    if (NW > 1) __syncthreads();
+    float gl = 0.f;
+    int id = 0;
+    if (wave == 0 && live) {
+      if (NW > 1 && lane < k && ((mask >> lane) & 1))
+        for (int p = 0; p < P; ++p) d += part[tg][lane][p];
       if (lane < k) dw[(long long)t * k + lane] = d;
       if (dlogits != nullptr) {
         float s = 0.f;  // sum_i w_i dw_i in slot order
@@ -224,31 +239,51 @@ __global__ __launch_bounds__(NW * 64) void combine_backward_kernel(
           s = fmaf(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wl), i)),
                    __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(d), i)), s);
         if (lane < k) {
-          g[lane] = wl * (d - s);
-          gid[lane] = ids[(long long)t * k + lane];
+          gl = wl * (d - s);
+          id = ids[(long long)t * k + lane];
+          if (NW > 1) {
+            gs[tg][lane] = gl;
+            gids[tg][lane] = id;
+          }
         }
       }
     }
-    __syncthreads();
-    if (dlogits != nullptr)
-      for (int e = threadIdx.x; e < E; e += NW * 64) {
+    if (NW > 1) __syncthreads();
+    if (dlogits != nullptr && live) {
+      float* out = dlogits + (long long)t * E;
+      for (int e = wave * 64 + lane; e < E; e += NW * 64) {
         float v = 0.f;
-        for (int i = 0; i < k; ++i) v += gid[i] == e ? g[i] : 0.f;
-        dlogits[(long long)t * E + e] = v;
+        for (int i = 0; i < k; ++i) {
+          const int at = NW > 1 ? gids[tg][i] : __builtin_amdgcn_readlane(id, i);
+          const float x = NW > 1 ? gs[tg][i] : __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(gl), i));
+          v += at == e ? x : 0.f;
+        }
+        out[e] = v;
       }
-    // part, g and gid are rewritten only after the next token's barriers: part before the first
-    // (its readers, wave 0, are past the second), g and gid between them
-    __syncthreads();
+    }
+    // part, gs and gids are rewritten only after the next tokens' barriers: part before the first
+    // (its readers, each group's wave 0, are past the second), gs and gids between them
+    if (NW > 1) __syncthreads();
   }
 }
 
-static unsigned token_grid(int T) { return (unsigned)(T < 65535 ? T : 65535); }
+// log2 of the waves a token's row of that many 16-byte chunks takes in dispatch and combine: 1, 2 or all 4 of a
+// workgroup.  32768 tokens of 512 bfloat16 values, 2 rows each: 16 and 17 us; with 4 waves each 25 and 28.
+static int waves_log2(long long chunks) { return chunks <= 64 ? 0 : chunks <= 128 ? 1 : 2; }
+
+// workgroups for T tokens, `tokens` in each at a time (the kernels' loops stay in 32 bits past the last one)
+static unsigned token_grid(int T, int tokens) {
+  const int n = (T + tokens - 1) / tokens, most = 65535 / tokens;
+  return (unsigned)(n < most ? n : most);
+}
 
 hipError_t launch_dispatch(const DispatchShape& d, const void* x, const int32_t* s2r, void* xs, hipStream_t s) {
   const long long es = dtype_bytes(d.dtype), row_bytes = (long long)d.H * es;
-  const unsigned chunks = (unsigned)((row_bytes + 4096 * kDispatchPer - 1) / (4096 * kDispatchPer));
-  dispatch_kernel<<<dim3(chunks, token_grid(d.T)), 256, 0, s>>>(
-      static_cast<const uint8_t*>(x), d.token_stride * es, s2r, d.T, d.k, d.max_rows, row_bytes,
+  const int wl = waves_log2((row_bytes + 15) / 16);
+  const long long cols = (1024 << wl) * kDispatchPer;
+  const dim3 grid((unsigned)((row_bytes + cols - 1) / cols), token_grid(d.T, 4 >> wl));
+  dispatch_kernel<<<grid, 256, 0, s>>>(
+      static_cast<const uint8_t*>(x), d.token_stride * es, s2r, d.T, d.k, d.max_rows, wl, row_bytes,
       static_cast<uint8_t*>(xs), d.row_stride * es);
   return hipGetLastError();
 }
@@ -256,9 +291,12 @@ hipError_t launch_dispatch(const DispatchShape& d, const void* x, const int32_t*
 template <typename T, bool WEIGHTED>
 static hipError_t combine_rows(const DispatchShape& d, const void* ys, const int32_t* s2r, const float* w, void* y,
                                hipStream_t s) {
-  constexpr int cols = 256 * Elem<T>::kVec;
-  combine_rows_kernel<T, WEIGHTED><<<dim3((unsigned)((d.H + cols - 1) / cols), token_grid(d.T)), 256, 0, s>>>(
-      static_cast<const T*>(ys), d.row_stride, s2r, w, d.T, d.k, d.max_rows, d.H, static_cast<T*>(y), d.token_stride);
+  constexpr int V = Elem<T>::kVec;
+  const int wl = waves_log2((d.H + V - 1) / V), cols = (64 << wl) * V;
+  const dim3 grid((unsigned)((d.H + cols - 1) / cols), token_grid(d.T, 4 >> wl));
+  combine_rows_kernel<T, WEIGHTED><<<grid, 256, 0, s>>>(
+      static_cast<const T*>(ys), d.row_stride, s2r, w, d.T, d.k, d.max_rows, wl, d.H, static_cast<T*>(y),
+      d.token_stride);
   return hipGetLastError();
 }
 
@@ -273,10 +311,19 @@ template <typename T>
 static hipError_t combine_backward(const DispatchShape& d, const void* dy, const void* ys, const int32_t* s2r,
                                    const float* w, void* dys, float* dw, const int32_t* ids, float* dlogits,
                                    hipStream_t s) {
-  combine_backward_kernel<T, 8><<<token_grid(d.T), 512, 0, s>>>(
-      static_cast<const T*>(dy), d.token_stride, static_cast<const T*>(ys), d.row_stride, s2r, w, d.T, d.k, d.max_rows,
-      d.H, static_cast<T*>(dys), dw, ids, d.E, dlogits);
-  return hipGetLastError();
+  const auto launch = [&](auto kern, int waves, int tokens) {
+    kern<<<token_grid(d.T, tokens), waves * tokens * 64, 0, s>>>(
+        static_cast<const T*>(dy), d.token_stride, static_cast<const T*>(ys), d.row_stride, s2r, w, d.T, d.k,
+        d.max_rows, d.H, static_cast<T*>(dys), dw, ids, d.E, dlogits);
+    return hipGetLastError();
+  };
+  // A wave takes a token by itself where the token's rows are at most 512 16-byte chunks (8 per lane) and there are
+  // tokens enough to fill the GPU: 32768 tokens of 512 bfloat16 values, 2 rows each, 27 instead of 99 us; 2048 tokens
+  // of 512, 4 rows each, 6.2 instead of 8.9.  (1024 tokens of 512, 8 rows each: 8.3, with eight waves 6.4; 16384
+  // tokens of 2048, 4 rows each: 122, with eight waves 115.)
+  const long long chunks = (long long)d.k * ((d.H + Elem<T>::kVec - 1) / Elem<T>::kVec);
+  if (d.T >= 2048 && chunks <= 512) return launch(combine_backward_kernel<T, 1, 4>, 1, 4);
+  return launch(combine_backward_kernel<T, 8, 1>, 8, 1);
 }
 
 hipError_t launch_combine_backward(const DispatchShape& d, const void* dy, const void* ys, const int32_t* s2r,

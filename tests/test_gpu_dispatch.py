@@ -238,6 +238,19 @@ def test_combine_backward(shape, dtype):
     assert torch.equal(dw2, dw) and torch.equal(dys2.cpu()[c.row], dys.cpu()[c.row])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", [
+    (2047, 512, 32, 0, 32, 8, 0, 0, 0, False), (2048, 512, 32, 0, 32, 8, 0, 0, 0, False),
+    (2051, 1025, 16, 3, 9, 4, 0, 3, 1, True), (2300, 1023, 8, 0, 8, 4, 5000, 0, 0, False),
+    (3001, 130, 64, 5, 40, 16, 0, 2, 1, False), (70001, 40, 6, 1, 4, 2, 0, 0, 0, False)],
+    ids=lambda s: f"T{s[0]}H{s[1]}k{s[5]}")
+def test_many_tokens_with_short_rows(shape, dtype):
+    """Several tokens share a workgroup; odd numbers of them leave its last groups without one."""
+    test_dispatch(shape, dtype)
+    test_dispatch_backward_and_combine(shape, dtype)
+    test_combine_backward(shape, dtype)
+
+
 def test_non_finite_rows_reach_only_their_token():
     """A row of NaN or infinities changes its own token only, also with a weight of 0 on another slot."""
     c = Case(20, 100, 8, 0, 8, 2, "bf16", seed=3)
