@@ -35,8 +35,8 @@ __device__ __forceinline__ v8i fp4_operand(uint4 q) {
 // Groups with few rows: the weights are what is read.  One workgroup takes 16 * NS weight rows of one
 // group; its NW waves take every NW-th 512-wide stretch of K, each lane straight from global memory into
 // the matrix instruction's registers (a weight is used once per 16 rows: nothing to gain from LDS), and
-// their partial sums meet in LDS, in wave order.  Rows go 16 or 32 at a time (MT = 1, 2); a group with
-// more is walked again, which the 256-row tiles below do better.  Bound by HBM: 4 rows for each of 32
+// their partial sums meet in LDS, in wave order.  Rows go 16, 32 or 64 at a time (MT); a group with
+// more is walked again, or by other workgroups (the grid's z).  Bound by HBM: 4 rows for each of 32
 // groups of 4096 x 7168 take 90 us, 5.5 TB/s of weights (5.6 by the layer's own decode FC1).
 template <typename T, int NW, int NS, int MAXR, int MT>
 __device__ __forceinline__ void gemm_rows(const Mxfp4GemmArgs& g, float (*part)[MAXR][NS * 16 + 1], int e, int n0, int m0,
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(NW * 64) void mxfp4_gemm_rows_kernel(Mxfp4GemmArgs 
   __shared__ float part[NW][MAXR][NS * 16 + 1];
   const int e = blockIdx.y, n0 = blockIdx.x * (NS * 16);
   const int2 rr = group_rows(g.offsets, e, g.rows);
-  for (int m0 = rr.x; m0 < rr.y; m0 += MAXR) {
+  for (int m0 = rr.x + blockIdx.z * MAXR; m0 < rr.y; m0 += gridDim.z * MAXR) {
     const int rows = rr.y - m0;
     if (rows <= 16) gemm_rows<T, NW, NS, MAXR, 1>(g, part, e, n0, m0, rr.y);
     else if (MAXR == 32 || rows <= 32) gemm_rows<T, NW, NS, MAXR, 2>(g, part, e, n0, m0, rr.y);
@@ -596,7 +596,13 @@ static hipError_t launch_tiles(const Mxfp4GemmArgs& g, hipStream_t s) {
 
 template <typename T, int NW, int NS, int MAXR>
 static hipError_t launch_rows(const Mxfp4GemmArgs& g, hipStream_t s) {
-  mxfp4_gemm_rows_kernel<T, NW, NS, MAXR><<<dim3((unsigned)((g.N + 16 * NS - 1) / (16 * NS)), (unsigned)g.groups), NW * 64, 0, s>>>(g);
+  const unsigned x = (unsigned)((g.N + 16 * NS - 1) / (16 * NS)), y = (unsigned)g.groups;
+  // few columns: the passes over rows spread over the grid up to 4096 waves, 16 per CU (one group may have all the
+  // rows).  5826 rows x 32 x 4768 in 7 groups 87 -> 9 us, 334 rows x 1744 x 6592 37 -> 14; with half the waves
+  // 1197 rows x 508 x 1728 in 7 groups 8.2 instead of 6.6 us, with twice as many 6.9.
+  const long long room = 4096 / NW / ((long long)x * y), most = (g.rows + MAXR - 1) / MAXR;
+  const unsigned z = (unsigned)(room < 1 ? 1 : room < most ? room : most);
+  mxfp4_gemm_rows_kernel<T, NW, NS, MAXR><<<dim3(x, y, z), NW * 64, 0, s>>>(g);
   return hipGetLastError();
 }
 
@@ -618,6 +624,9 @@ static bool use_tiles(const Mxfp4GemmArgs& g) {
 template <typename T>
 static hipError_t launch(const Mxfp4GemmArgs& g, int variant, hipStream_t s) {
   if (variant == 1 || (variant < 0 && use_tiles(g))) return launch_tiles<T, 256, 256, 8, 64, 128>(g, s);
+  // K within one 512-wide stretch: nothing to split over waves, so each is a workgroup (5838 rows x 1027 x 96 in
+  // 4 groups 12 against 22 us, 8241 rows x 625 x 160 in 24 groups 9 against 15 us)
+  if (g.K <= 512) return launch_rows<T, 1, 2, 32>(g, s);
   // up to 16 rows a group: half the registers, twice the waves (32 groups of 7168 x 2048, 4 rows each: 43
   // against 55 us); above: 64 rows a pass (one group of 8192 x 8192, 64 rows: 16 against 27 us)
   if ((long long)g.rows <= 16LL * g.groups) {

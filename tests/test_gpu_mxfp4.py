@@ -217,6 +217,15 @@ def test_product_exact(sizes, N, K, variant):
     assert torch.equal(p.run().double(), p.ref())
 
 
+@pytest.mark.parametrize("variant", [-1, 0])
+@pytest.mark.parametrize("sizes,N,K", [([9000], 2, 32), ([700, 0, 65, 3], 22, 64), ([130, 1000], 33, 512),
+                                       ([1, 300, 5], 70, 544), ([1000, 600, 64], 40, 1056), ([5, 1], 5000, 96)])
+def test_product_rows_spread_over_workgroups(sizes, N, K, variant):
+    """Few columns, or K of one stretch: a group's rows go to several workgroups, or single waves."""
+    p = Product(sizes, N, K, rows=sum(sizes) + 3, seed=K + N, pad=1, variant=variant)
+    assert torch.equal(p.run().double(), p.ref())
+
+
 @pytest.mark.parametrize("variant", [0, 1])
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("sizes,N,K", PRODUCTS[1:9:2] + [([512, 256], 512, 1024)], ids=IDS[1:9:2] + ["whole"])
