@@ -33,20 +33,22 @@ __device__ __forceinline__ uint64_t token_rows(const int32_t* __restrict__ s2r, 
   return __ballot((unsigned)row < (unsigned)max_rows);
 }
 
-// grid (column chunks, tokens): 256 threads on 1, 2 or 4 tokens, kDispatchPer 16-byte chunks of a row each, read once
+// grid (column chunks, tokens): 256 threads on 1, 2 or 4 tokens, PER 16-byte chunks of a row each, read once
 // and stored to every row the token has (a kernel by rows would read a token up to k times).  128 tokens of
-// 14 KB, 128 rows: 3.4 us, the latency of map -> row -> store.
-constexpr int kDispatchPer = 2;
-
+// 14 KB, 125 rows: 2.5 us, the latency of map -> row -> store; 4096 tokens, 4136 rows: 16 us, 7.3 TB/s from the
+// caches; 32768 tokens, 32586 rows: 151 us, 6.2 TB/s.
+template <int PER>
 __global__ __launch_bounds__(256) void dispatch_kernel(const uint8_t* __restrict__ x, long long x_pitch,
                                                        const int32_t* __restrict__ s2r, int T, int k, int max_rows,
                                                        int waves_log2, long long row_bytes, uint8_t* __restrict__ xs,
                                                        long long xs_pitch) {
   const int lane = threadIdx.x & 63, lanes = 64 << waves_log2, pitch = lanes * 16;
-  const long long c0 = ((long long)blockIdx.x * (lanes * kDispatchPer) + (threadIdx.x & (lanes - 1))) * 16;
+  const long long c0 = ((long long)blockIdx.x * (lanes * PER) + (threadIdx.x & (lanes - 1))) * 16;
   // the row's last, partial chunk, where it is one of this lane's
-  const long long whole = row_bytes & ~15LL, last = whole == c0 || whole == c0 + pitch ? whole : row_bytes;
-  static_assert(kDispatchPer == 2, "");
+  long long last = row_bytes;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (c0 + i * pitch == (row_bytes & ~15LL)) last = c0 + i * pitch;
   const int tg = __builtin_amdgcn_readfirstlane(threadIdx.x >> (6 + waves_log2)), tokens = 4 >> waves_log2;
   for (int t0 = blockIdx.y * tokens; t0 < T; t0 += gridDim.y * tokens) {
     const int t = t0 + tg;
@@ -55,16 +57,16 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const uint8_t* __restrict
     uint64_t mask = token_rows(s2r, t, k, k, max_rows, lane, row);
     if (mask == 0) continue;
     const uint8_t* src = x + (long long)t * x_pitch;
-    u32x4 v[kDispatchPer];
+    u32x4 v[PER];
 #pragma unroll
-    for (int i = 0; i < kDispatchPer; ++i)
+    for (int i = 0; i < PER; ++i)
       if (c0 + i * pitch + 16 <= row_bytes) v[i] = load16(src + c0 + i * pitch);
     while (mask) {
       const int j = __builtin_ctzll(mask);
       mask &= mask - 1;
       uint8_t* dst = xs + (long long)__builtin_amdgcn_readlane(row, j) * xs_pitch;
 #pragma unroll
-      for (int i = 0; i < kDispatchPer; ++i)
+      for (int i = 0; i < PER; ++i)
         if (c0 + i * pitch + 16 <= row_bytes) store16(dst + c0 + i * pitch, v[i]);
       if (last < row_bytes)
         for (long long b = last; b < row_bytes; ++b) dst[b] = src[b];
@@ -280,12 +282,17 @@ static unsigned token_grid(int T, int tokens) {
 hipError_t launch_dispatch(const DispatchShape& d, const void* x, const int32_t* s2r, void* xs, hipStream_t s) {
   const long long es = dtype_bytes(d.dtype), row_bytes = (long long)d.H * es;
   const int wl = waves_log2((row_bytes + 15) / 16);
-  const long long cols = (1024 << wl) * kDispatchPer;
-  const dim3 grid((unsigned)((row_bytes + cols - 1) / cols), token_grid(d.T, 4 >> wl));
-  dispatch_kernel<<<grid, 256, 0, s>>>(
-      static_cast<const uint8_t*>(x), d.token_stride * es, s2r, d.T, d.k, d.max_rows, wl, row_bytes,
-      static_cast<uint8_t*>(xs), d.row_stride * es);
-  return hipGetLastError();
+  const auto launch = [&](auto kern, int per) {
+    const long long cols = (1024LL << wl) * per;
+    const dim3 grid((unsigned)((row_bytes + cols - 1) / cols), token_grid(d.T, 4 >> wl));
+    kern<<<grid, 256, 0, s>>>(static_cast<const uint8_t*>(x), d.token_stride * es, s2r, d.T, d.k, d.max_rows, wl,
+                              row_bytes, static_cast<uint8_t*>(xs), d.row_stride * es);
+    return hipGetLastError();
+  };
+  // few tokens: one chunk per thread, as many workgroups as can be (128 tokens of 14 KB 2.5 us, with four 4.0;
+  // 1024: 5.8 and 6.0); many: a workgroup per 16 KB, which most tokens of an expert share leave at once (4096
+  // tokens of 14 KB, 249 rows: 4.8 us, with one chunk 9.1; 4136 rows: 16.3 and 17.5)
+  return d.T <= 1024 ? launch(dispatch_kernel<1>, 1) : launch(dispatch_kernel<4>, 4);
 }
 
 template <typename T, bool WEIGHTED>

@@ -164,9 +164,11 @@ def test_dispatch(shape, dtype):
     c.untouched(buf, c.cap, c.H + 2 * c.pad, c.row)
 
 
-@pytest.mark.parametrize("nbytes,shift", [(1, 0), (15, 1), (224, 0), (3584, 0), (8193, 3)])
-def test_dispatch_bytes(nbytes, shift):
-    T, E, k = 37, 16, 4
+@pytest.mark.parametrize("nbytes,shift,T", [(1, 0, 37), (15, 1, 37), (224, 0, 37), (3584, 0, 37), (8193, 3, 37),
+                                            (1, 0, 1100), (1030, 0, 1100), (2047, 1, 1025), (5000, 0, 1100),
+                                            (16384, 0, 1025), (20005, 5, 1030)])
+def test_dispatch_bytes(nbytes, shift, T):
+    E, k = 16, 4
     ids = make_ids(T, E, k, 5)
     s2r = torch.from_numpy(sort_ref(ids, 4, 9)[3])
     g = torch.Generator().manual_seed(1)
