@@ -490,11 +490,19 @@ __global__ __launch_bounds__(512) void permute_scatter_kernel(const int32_t* __r
   if (SELF) {
     const int lanes = 1 << lanes_log2, b = tid & (lanes - 1), step = 512 >> lanes_log2;
     int all = 0, before = 0;
-#pragma unroll 8
-    for (int c = tid >> lanes_log2; c < (int)gridDim.x; c += step) {
-      const int v = chunk_cnt[c * NB + (b < NB ? b : 0)];
-      all += v;
-      before += c < (int)blockIdx.x ? v : 0;
+    for (int c0 = tid >> lanes_log2; c0 < (int)gridDim.x; c0 += 8 * step) {  // eight loads in flight
+      int v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = c0 + i * step;
+        v[i] = chunk_cnt[(c < (int)gridDim.x ? c : (int)gridDim.x - 1) * NB + (b < NB ? b : 0)];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = c0 + i * step;
+        all += c < (int)gridDim.x ? v[i] : 0;
+        before += c < (int)blockIdx.x ? v[i] : 0;
+      }
     }
     part[0][tid] = all;
     part[1][tid] = before;
