@@ -426,7 +426,7 @@ typedef struct {
   int32_t a_scale_layout;  /* moe_sf_layout; row-major needs K a multiple of 128 */
   int32_t b_scale_layout;
   int32_t variant;         /* -1 = by size; 0 = 16-column tiles straight from memory (few rows);
-                              1 = 256 x 256 tiles */
+                              1 = 256 x 256 tiles; 2 = 128 x 128 tiles */
   int64_t out_stride;      /* elements between rows of C; 0 = N */
 } moe_mxfp4_gemm_desc;
 

@@ -710,7 +710,7 @@ moe_status moe_mxfp4_gemm(const moe_mxfp4_gemm_desc* d, const uint8_t* a, const 
   if (moe_status st = check_mx_float(d->out_dtype)) return st;
   if (moe_status st = check_mx_layout(d->a_scale_layout)) return st;
   if (moe_status st = check_mx_layout(d->b_scale_layout)) return st;
-  if (d->variant < -1 || d->variant > 1) return fail(MOE_ERR_INVALID_DESC, "variant %d unknown", d->variant);
+  if (d->variant < -1 || d->variant > 2) return fail(MOE_ERR_INVALID_DESC, "variant %d unknown", d->variant);
   if (d->out_stride != 0 && (d->out_stride < d->n || d->out_stride > kMaxStride))
     return fail(MOE_ERR_INVALID_DESC, "out_stride %lld neither 0 nor in [n, 2^40]", (long long)d->out_stride);
   if (d->k % 128 && (d->a_scale_layout == MOE_SF_ROW_MAJOR || d->b_scale_layout == MOE_SF_ROW_MAJOR))

@@ -139,7 +139,9 @@ __global__ __launch_bounds__(NW * 64) void mxfp4_gemm_rows_kernel(Mxfp4GemmArgs 
 }
 
 // ---------------------------------------------------------------------------------------
-// Tiles of BM rows x BN columns for groups with many rows.
+// Tiles of BM rows x BN columns: 256 x 256 by eight waves of 64 x 128 where there are many, 128 x 128 by four waves of
+// 32 x 128, two workgroups on a CU, where they would fill the GPU badly (the results of one are then stored while
+// the other multiplies; its waves read 5 fragments for 4 instructions, where the large ones read 6 for 8).
 //
 // K advances 256 values a stage: 128 bytes (a cache line) of codes per operand row, brought from
 // global memory straight into one of two LDS slots, and two scale words per row, into one of four.
@@ -195,8 +197,8 @@ template <typename T, int BM, int BN, int NW, int WTM, int WTN>
 __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmArgs g) {
   using C = TileCfg<BM, BN, NW, WTM, WTN>;
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  // the first row tile of each group [groups + 1], unsigned: groups that overlap (offsets that are not
-  // what they should be) have at most 1024 * 2^22 tiles
+  // the first row tile of each group [groups + 1], unsigned: where groups overlap (offsets that are not what they
+  // should be), 512 of 1024 can have all of at most 2^30 rows, 2^32 tiles of 128 rows, which count as none
   unsigned* s_plan = reinterpret_cast<unsigned*>(lds + C::kPlan);
   int* s_lo = reinterpret_cast<int*>(s_plan + g.groups + 1);  // [groups] first row
   int* s_hi = s_lo + g.groups;                                // [groups] end
@@ -586,10 +588,11 @@ static hipError_t launch_tiles(const Mxfp4GemmArgs& g, hipStream_t s) {
     if (e != hipSuccess) return e;
     ready.fetch_or(bit, std::memory_order_acq_rel);
   }
-  // at most this many tiles; one workgroup per CU, in whole rows of 8 XCDs
+  // at most this many tiles; as many workgroups as the LDS lets a CU hold (with up to some 600 groups), in whole
+  // rows of 8 XCDs
   const long long most = (((long long)g.rows + (long long)g.groups * (BM - 1)) / BM) * ((g.N + BN - 1) / BN);
-  const long long cus = device_cus();
-  const unsigned grid = (unsigned)(((most < cus ? most : cus) + 7) / 8 * 8);
+  const long long room = (long long)device_cus() * (160 * 1024 / (C::kPlan + 8 * 1024));
+  const unsigned grid = (unsigned)(((most < room ? most : room) + 7) / 8 * 8);
   kern<<<dim3(grid), dim3(C::NT), bytes, s>>>(g);
   return hipGetLastError();
 }
@@ -606,24 +609,39 @@ static hipError_t launch_rows(const Mxfp4GemmArgs& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rows kernel or tiles, by an estimate of both in microseconds from the sizes alone (the groups' rows are on
-// the device: their average stands for them).  The tile kernel takes 8 us a tile plus 1.1 us for each of its
-// stages, in rounds of one tile per CU, however few rows a tile has; the rows kernel's time goes with the
-// multiplications of its 16-row tiles.  Measured, rows / tiles: one group of 8192 x 8192: 64 rows 16 / 44 us,
-// 128 rows 28 / 45 us, 200 rows 47 / 46 us; 8 groups of 4096 x 4096: 32 rows each 20 / 26 us, 64 rows
-// 35 / 27 us; 32 groups of 4096 x 7168: 4 rows each 90 / 99 us, 32 rows 138 / 105 us.
-static bool use_tiles(const Mxfp4GemmArgs& g) {
-  const double avg = (g.rows + g.groups - 1) / g.groups;
-  const double cus = device_cus(), stages = (g.K + 255) / 256;
-  const double tiles = (double)g.groups * ((g.N + 255) / 256) * (double)((int)(avg + 255) / 256);
-  const double tile_us = (double)(long long)((tiles + cus - 1) / cus) * (8.0 + 1.1 * stages);
-  const double rows_us = 5.0 + 3.5e-9 * (double)((int)(avg + 15) / 16 * 16) * g.groups * g.N * g.K;
-  return rows_us > tile_us;
+// Rows kernel (0), 256 x 256 tiles (1) or 128 x 128 tiles (2), by estimates in microseconds from the sizes alone
+// (the groups' rows are on the device: their average stands for them).  Each is the larger of the weights' bytes at
+// 5.5 TB/s (a kernel whose tiles are all resident at once reaches less) and of its own work: the rows kernel's
+// latency grows with K and its time with the multiplications of its 16-row tiles, the tile kernels take their tiles
+// in rounds, each a fixed time plus one for each stage of 256 along K, the longer the fuller the GPU is.  The
+// figures are fitted to 303 shapes (1 to 32 groups of 1 to 2048 rows, nine N x K from 256 x 256 to 8192 x 8192), where
+// the choice is on average 0.2% off the fastest.  Measured, rows / 256 / 128: one group of 8192 x 8192: 64 rows
+// 15 / 44 / 24 us, 200 rows 42 / 46 / 25 us; 8 groups of 4096 x 4096: 64 rows each 35 / 26 / 16 us; 32 groups of
+// 4096 x 7168: 4 rows each 93 / 96 / 85 us, 32 rows 133 / 102 / 89 us, 128 rows 366 / 119 / 130 us; 8192 x 8192 x 8192
+// - / 265 / 344 us.
+static int choose(const Mxfp4GemmArgs& g) {
+  const double avg = (double)((g.rows + g.groups - 1) / g.groups), cus = device_cus(), stages = (g.K + 255) / 256;
+  const double weights_us = 0.53 / 5.5e6 * g.groups * g.N * g.K;
+  const auto tiles_us = [&](int size, double slots, double fixed, double stage_idle, double stage_full) {
+    const double m = (double)(((int)avg + size - 1) / size), n = (double)((g.N + size - 1) / size);
+    const double full = g.groups * m * n / slots, rounds = __builtin_ceil(full);
+    const double stage = stage_idle + (stage_full - stage_idle) * (full < 1 ? full : 1);
+    const double bytes_us = weights_us * (rounds <= 1 ? 1.15 : 1.0), work_us = rounds * (fixed + stage * stages);
+    return bytes_us > work_us ? bytes_us : work_us;
+  };
+  const double base_us = 5.3 + 0.5e-3 * g.K;
+  const double rows_us = (weights_us > base_us ? weights_us : base_us) +
+                         2.7e-9 * (avg <= 16 ? avg : (double)(((int)avg + 15) / 16 * 16)) * g.groups * g.N * g.K;
+  const double us256 = tiles_us(256, cus, 7.1, 0.98, 1.7), us128 = tiles_us(128, 2 * cus, 5.5, 0.77, 1.3);
+  if (rows_us <= us256 && rows_us <= us128) return 0;
+  return us256 <= us128 ? 1 : 2;
 }
 
 template <typename T>
 static hipError_t launch(const Mxfp4GemmArgs& g, int variant, hipStream_t s) {
-  if (variant == 1 || (variant < 0 && use_tiles(g))) return launch_tiles<T, 256, 256, 8, 64, 128>(g, s);
+  if (variant < 0) variant = choose(g);
+  if (variant == 1) return launch_tiles<T, 256, 256, 8, 64, 128>(g, s);
+  if (variant == 2) return launch_tiles<T, 128, 128, 4, 32, 128>(g, s);
   // K within one 512-wide stretch: nothing to split over waves, so each is a workgroup (5838 rows x 1027 x 96 in
   // 4 groups 12 against 22 us, 8241 rows x 625 x 160 in 24 groups 9 against 15 us)
   if (g.K <= 512) return launch_rows<T, 1, 2, 32>(g, s);

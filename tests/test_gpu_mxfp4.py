@@ -208,12 +208,18 @@ PRODUCTS = [  # sizes, N, K
 IDS = [f"G{len(s)}R{sum(s)}N{n}K{k}" for s, n, k in PRODUCTS]
 
 
-@pytest.mark.parametrize("variant", [-1, 0, 1])
+@pytest.mark.parametrize("variant", [-1, 0, 1, 2])
 @pytest.mark.parametrize("sizes,N,K", PRODUCTS, ids=IDS)
 def test_product_exact(sizes, N, K, variant):
     """Scales in {1/2, 1, 2}: every product is a multiple of 2^-4 and every sum below 2^20, so float32 sums in any
     order are exact, and so must the results be.  Rows behind the last group stay as they were."""
     p = Product(sizes, N, K, rows=sum(sizes) + 5, seed=K + N, pad=3, shift=1, variant=variant)
+    assert torch.equal(p.run().double(), p.ref())
+
+
+@pytest.mark.parametrize("variant", [1, 2])
+def test_product_more_tiles_than_workgroups(variant):
+    p = Product([4000, 0, 700], 4100, 288, rows=4701, seed=5, variant=variant)
     assert torch.equal(p.run().double(), p.ref())
 
 
@@ -226,7 +232,7 @@ def test_product_rows_spread_over_workgroups(sizes, N, K, variant):
     assert torch.equal(p.run().double(), p.ref())
 
 
-@pytest.mark.parametrize("variant", [0, 1])
+@pytest.mark.parametrize("variant", [0, 1, 2])
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("sizes,N,K", PRODUCTS[1:9:2] + [([512, 256], 512, 1024)], ids=IDS[1:9:2] + ["whole"])
 def test_product_rounding(sizes, N, K, out, variant):
@@ -239,7 +245,7 @@ def test_product_rounding(sizes, N, K, out, variant):
     assert ((p.run().double() - ref).abs() <= tol).all()
 
 
-@pytest.mark.parametrize("variant", [0, 1])
+@pytest.mark.parametrize("variant", [0, 1, 2])
 @pytest.mark.parametrize("la", ["rows", "packed"])
 @pytest.mark.parametrize("lb", ["rows", "packed"])
 @pytest.mark.parametrize("sizes,N,K", [([3, 9], 50, 640), ([300, 10], 300, 1152)], ids=["few", "many"])
@@ -248,7 +254,7 @@ def test_product_scale_layouts(sizes, N, K, la, lb, variant):
     assert torch.equal(p.run().double(), p.ref())
 
 
-@pytest.mark.parametrize("variant", [0, 1])
+@pytest.mark.parametrize("variant", [0, 1, 2])
 @pytest.mark.parametrize("rows", [7, 600])
 def test_product_nan_scales(rows, variant):
     """Scale byte 255 makes its row, or its column of its group, NaN, and nothing else."""
@@ -263,7 +269,7 @@ def test_product_nan_scales(rows, variant):
     assert torch.equal(got.double()[~want], ref[~want])
 
 
-@pytest.mark.parametrize("variant", [0, 1])
+@pytest.mark.parametrize("variant", [0, 1, 2])
 @pytest.mark.parametrize("rows", [7, 600])
 def test_product_garbage_past_k(rows, variant):
     """The padding of the last packed scale word is not part of the sum, whatever it holds."""
@@ -274,7 +280,7 @@ def test_product_garbage_past_k(rows, variant):
     assert torch.equal(p.run((a, asf, b, bsf, off)).double(), p.ref())
 
 
-@pytest.mark.parametrize("variant", [0, 1])
+@pytest.mark.parametrize("variant", [0, 1, 2])
 @pytest.mark.parametrize("rows", [20, 700])
 def test_product_offsets_are_cut_to_the_rows(rows, variant):
     """Offsets outside [0, rows] or descending do not lead outside the tensors."""
@@ -291,7 +297,7 @@ def test_product_offsets_are_cut_to_the_rows(rows, variant):
     assert torch.equal(c.cpu().double(), torch.from_numpy(av @ bv[0].T))
 
 
-@pytest.mark.parametrize("variant", [0, 1])
+@pytest.mark.parametrize("variant", [0, 1, 2])
 @pytest.mark.parametrize("rows", [3, 300])
 def test_plain_product_without_offsets(rows, variant):
     p = Product([rows], 100, 512, seed=6, variant=variant)
@@ -299,7 +305,7 @@ def test_plain_product_without_offsets(rows, variant):
     assert torch.equal(p.run((a, asf, b, bsf, None)).double(), p.ref())
 
 
-@pytest.mark.parametrize("variant", [0, 1])
+@pytest.mark.parametrize("variant", [0, 1, 2])
 def test_product_many_groups(variant):
     """1024 groups, most of them empty: the tile plan's largest size."""
     r = np.random.RandomState(3)
@@ -309,7 +315,7 @@ def test_product_many_groups(variant):
     assert torch.equal(p.run().double(), p.ref())
 
 
-@pytest.mark.parametrize("variant", [0, 1])
+@pytest.mark.parametrize("variant", [0, 1, 2])
 def test_products_on_two_streams_at_once(variant):
     ps = [Product([200, 0, 313], 300, 2048, seed=s, variant=variant) for s in (1, 2)]
     args = [p.args() for p in ps]
@@ -324,7 +330,7 @@ def test_products_on_two_streams_at_once(variant):
         assert torch.equal(c.cpu().double(), p.ref())
 
 
-@pytest.mark.parametrize("variant", [0, 1])
+@pytest.mark.parametrize("variant", [0, 1, 2])
 def test_product_scales_on_a_4_byte_boundary(variant):
     p = Product([90], 64, 256, seed=3, la="rows", lb="rows", variant=variant)
     a, asf, b, bsf, off = p.args()
