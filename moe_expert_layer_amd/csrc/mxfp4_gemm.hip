@@ -170,7 +170,9 @@ __global__ __launch_bounds__(NW * 64) void mxfp4_gemm_rows_kernel(Mxfp4GemmArgs 
 // wave, four waves (656 us on the last shape: one wave a SIMD waits for its own loads to issue); half-line
 // stages, four of them (472 us, twice the L2 requests); results stored from the registers, 32 bytes a row
 // at a time (680 against 525 us on the first shape); lines of later stages touched ahead, by every wave
-// (3% slower) or by waves with no other loads.
+// (3% slower) or by waves with no other loads; 128 x 128 tiles with four stages in flight, one workgroup on a CU (8
+// groups of 4096 x 7168, 64 rows each: 27 against 34 us, but the same where the weights are not what is waited for:
+// there a stage is 80 KB of fragments read from LDS and 32 KB written, 0.55 us).
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
