@@ -249,7 +249,7 @@ __global__ __launch_bounds__(1024) void permute_scan_kernel(const int32_t* __res
   if (lane == 0 && b < EL) counts[b] = carry;
 }
 
-// Everything in one workgroup when the slots are few (decode-sized calls): histogram,
+// Everything in one workgroup when the slots are few and the local experts 64 or more: histogram,
 // scans, tile plan and the stable scatter, in rounds of 1024 slots.
 __global__ __launch_bounds__(1024) void permute_small_kernel(const int32_t* __restrict__ ids, int nslots, int e0,
                                                              int EL, int bm, int32_t* __restrict__ counts,
@@ -286,20 +286,8 @@ __global__ __launch_bounds__(1024) void permute_small_kernel(const int32_t* __re
     mt[b] = (a[b] + bm - 1) / bm;
   }
   __syncthreads();
-  if (NB <= 64) {  // one wave scans both (entries past NB are zero and stay unused)
-    if (wave == 0) {
-      const int v = lane < NB ? a[lane] : 0, m = lane < NB ? mt[lane] : 0;
-      const int iv = wave_inclusive_scan(v), im = wave_inclusive_scan(m);
-      if (lane < NB) {
-        a[lane] = iv - v;
-        mt[lane] = im - m;
-      }
-    }
-    __syncthreads();
-  } else {
-    block_exclusive_scan_2048(a);
-    block_exclusive_scan_2048(mt);
-  }
+  block_exclusive_scan_2048(a);
+  block_exclusive_scan_2048(mt);
   for (int b = tid; b < NB; b += 1024) {
     offsets[b] = a[b];
     plan[b] = mt[b];
