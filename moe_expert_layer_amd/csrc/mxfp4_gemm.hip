@@ -616,7 +616,7 @@ static hipError_t launch_rows(const Mxfp4GemmArgs& g, hipStream_t s) {
 // 5.5 TB/s (a kernel whose tiles are all resident at once reaches less) and of its own work: the rows kernel's
 // latency grows with K and its time with the multiplications of its 16-row tiles, the tile kernels take their tiles
 // in rounds, each a fixed time plus one for each stage of 256 along K, the longer the fuller the GPU is.  The
-// figures are fitted to 501 shapes (1 to 32 groups of 1 to 2048 rows, nine N x K from 256 x 256 to 8192 x 8192), where
+// figures are fitted to 501 shapes (1 to 32 groups of 1 to 2048 rows, nine N x K from 300 x 64 to 8192 x 8192), where
 // the choice is on average 0.2% off the fastest.  Measured, rows / 256 / 128: one group of 8192 x 8192: 64 rows
 // 15 / 44 / 24 us, 200 rows 42 / 46 / 25 us; 8 groups of 4096 x 4096: 64 rows each 35 / 26 / 16 us; 32 groups of
 // 4096 x 7168: 4 rows each 93 / 96 / 85 us, 32 rows 133 / 102 / 89 us, 128 rows 366 / 119 / 130 us; 8192 x 8192 x 8192
