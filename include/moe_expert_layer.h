@@ -326,7 +326,8 @@ moe_status moe_unpack_scales(int32_t rows, int32_t groups, const int32_t* packed
  *     topk_w, dw [T, k] and dlogits [T, E_tot] are float32 and dense, topk_ids int32 [T, k].
  *   - Sums are taken in float32 in slot order and rounded once (to nearest even) to the dtype;
  *     there are no atomics, so results are the same from run to run.  A slot without a row is
- *     left out of the sums whatever its weight; a row with a weight of 0 is read (0 * NaN = NaN).
+ *     left out of the sums over rows (dx, y and sum_i) whatever its weight, which is used for its
+ *     own term of dlogits alone; a row with a weight of 0 is read (0 * NaN = NaN).
  *   - Rows that no slot owns, and the elements between H and the stride, are left as they were.
  *   - slot_to_row comes from moe_sort_tokens or moe_route_permute; a map entry outside
  *     [0, max_rows) counts as no row, so rows past the caller's tensors are dropped.  Two slots

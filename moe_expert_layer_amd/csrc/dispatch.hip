@@ -236,10 +236,12 @@ __global__ __launch_bounds__(NW * G * 64) void combine_backward_kernel(
         for (int p = 0; p < P; ++p) d += part[tg][lane][p];
       if (lane < k) dw[(long long)t * k + lane] = d;
       if (dlogits != nullptr) {
-        float s = 0.f;  // sum_i w_i dw_i in slot order
-        for (int i = 0; i < k; ++i)
+        float s = 0.f;  // sum_i w_i dw_i in slot order, over the slots with a row: w may be anything on the others
+        for (uint64_t m = mask; m; m &= m - 1) {
+          const int i = __builtin_ctzll(m);
           s = fmaf(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wl), i)),
                    __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(d), i)), s);
+        }
         if (lane < k) {
           gl = wl * (d - s);
           id = ids[(long long)t * k + lane];

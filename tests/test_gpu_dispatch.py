@@ -266,6 +266,32 @@ def test_non_finite_rows_reach_only_their_token():
     assert torch.equal(torch.isfinite(y.float()).all(1).cpu(), ~bad)
 
 
+@pytest.mark.parametrize("T,H,k", [(37, 520, 4), (2100, 40, 8), (2049, 300, 16)])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_weights_of_slots_without_a_row_are_not_used(T, H, k, bad):
+    """Slots of experts elsewhere, or past the rows, may have weights that are not finite: dys, dw, y and the gradients
+    of the other logits are bit for bit what they are with a weight of 0 there."""
+    c = Case(T, H, 24, 5, 9, k, "bf16", max_rows=T * k // 4, seed=T)
+    assert (c.offsets[-1] > c.cap) and not c.has.all()
+    ids, s2r = c.ids.cuda(), c.s2r.cuda()
+    x, ys = c.tokens(c.x)[0], c.rows(c.ys)[0]
+
+    def run(fill):
+        w = torch.where(c.has.reshape(T, k), c.w, torch.full((), fill)).cuda()
+        y = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+        dys, dw, dl = torch.zeros_like(ys), torch.zeros(T, k, device="cuda"), torch.zeros(T, c.E, device="cuda")
+        B.moe_combine(c.desc, ys, s2r, w, y)
+        B.moe_combine_backward(c.desc, x, ys, s2r, w, dys, dw, topk_ids=ids, dlogits=dl)
+        return y, dys, dw, dl
+
+    (y, dys, dw, dl), (y0, dys0, dw0, dl0) = run(bad), run(0.0)
+    assert torch.equal(y, y0) and torch.equal(dys, dys0) and torch.equal(dw, dw0)
+    # a slot's own logit is weighted with its own weight; every other one is not touched by it
+    own = torch.zeros(T, c.E, dtype=torch.bool)
+    own[c.tok.new_tensor(np.repeat(np.arange(T), k))[~c.has], c.ids.reshape(-1)[~c.has].long()] = True
+    assert torch.equal(dl.cpu()[~own], dl0.cpu()[~own])
+
+
 def test_gradient_of_the_router_against_differences():
     """dlogits, dx and dw against central differences of the float64 formula of loss = <g, combine(dispatch(x))>
     through the softmax over the chosen logits."""
