@@ -615,25 +615,30 @@ static hipError_t launch_rows(const Mxfp4GemmArgs& g, hipStream_t s) {
 // (the groups' rows are on the device: their average stands for them).  Each is the larger of the weights' bytes at
 // 5.5 TB/s (a kernel whose tiles are all resident at once reaches less) and of its own work: the rows kernel's
 // latency grows with K and its time with the multiplications of its 16-row tiles, the tile kernels take their tiles
-// in rounds, each a fixed time plus one for each stage of 256 along K, the longer the fuller the GPU is.  The
-// figures are fitted to 501 shapes (1 to 32 groups of 1 to 2048 rows, nine N x K from 300 x 64 to 8192 x 8192), where
-// the choice is on average 0.2% off the fastest.  Measured, rows / 256 / 128: one group of 8192 x 8192: 64 rows
-// 15 / 44 / 24 us, 200 rows 42 / 46 / 25 us; 8 groups of 4096 x 4096: 64 rows each 35 / 26 / 16 us; 32 groups of
-// 4096 x 7168: 4 rows each 93 / 96 / 85 us, 32 rows 133 / 102 / 89 us, 128 rows 366 / 119 / 130 us; 8192 x 8192 x 8192
-// - / 265 / 344 us.
+// in rounds, each a fixed time plus one for each stage of 256 along K, the longer the fuller the GPU is.  Where there
+// are fewer rows than groups, only as many groups as rows count, and the rows kernel needs at least the time that
+// its workgroups without rows take to come and go, 0.25 us a thousand (1 row in 256 groups of 7168 x 2048: 18 us,
+// with 128 x 128 tiles 11; in 32 groups of 4096 x 7168 9.6 and 21 us).  The figures are fitted to 501 shapes (1 to 32
+// groups of 1 to 2048 rows, nine N x K from 300 x 64 to 8192 x 8192), where the choice is on average 0.2% off the
+// fastest, as it is on 166 with fewer rows than groups (2 to 1024 of them), spread over the groups.  Measured, rows /
+// 256 / 128: one group of 8192 x 8192: 64 rows 15 / 44 / 24 us, 200 rows 42 / 46 / 25 us; 8 groups of 4096 x 4096: 64
+// rows each 35 / 26 / 16 us; 32 groups of 4096 x 7168: 4 rows each 93 / 96 / 85 us, 32 rows 133 / 102 / 89 us, 128 rows
+// 366 / 119 / 130 us; 8192 x 8192 x 8192 - / 265 / 344 us.
 static int choose(const Mxfp4GemmArgs& g) {
-  const double avg = (double)((g.rows + g.groups - 1) / g.groups), cus = device_cus(), stages = (g.K + 255) / 256;
-  const double weights_us = 0.53 / 5.5e6 * g.groups * g.N * g.K;
+  const int active = g.rows < g.groups ? g.rows : g.groups;  // groups that can have rows
+  const double avg = (double)((g.rows + active - 1) / active), cus = device_cus(), stages = (g.K + 255) / 256;
+  const double weights_us = 0.53 / 5.5e6 * active * g.N * g.K;
   const auto tiles_us = [&](int size, double slots, double fixed, double stage_idle, double stage_full) {
     const double m = (double)(((int)avg + size - 1) / size), n = (double)((g.N + size - 1) / size);
-    const double full = g.groups * m * n / slots, rounds = __builtin_ceil(full);
+    const double full = active * m * n / slots, rounds = __builtin_ceil(full);
     const double stage = stage_idle + (stage_full - stage_idle) * (full < 1 ? full : 1);
     const double bytes_us = weights_us * (rounds <= 1 ? 1.15 : 1.0), work_us = rounds * (fixed + stage * stages);
     return bytes_us > work_us ? bytes_us : work_us;
   };
-  const double base_us = 5.3 + 0.5e-3 * g.K;
+  const double empty_us = 3.5 + 0.25e-3 * (g.groups - active) * ((g.N + 31) / 32), fixed_us = 5.3 + 0.5e-3 * g.K;
+  const double base_us = empty_us > fixed_us ? empty_us : fixed_us;
   const double rows_us = (weights_us > base_us ? weights_us : base_us) +
-                         2.7e-9 * (avg <= 16 ? avg : (double)(((int)avg + 15) / 16 * 16)) * g.groups * g.N * g.K;
+                         2.7e-9 * (avg <= 16 ? avg : (double)(((int)avg + 15) / 16 * 16)) * active * g.N * g.K;
   const double us256 = tiles_us(256, cus, 7.1, 0.98, 1.7), us128 = tiles_us(128, 2 * cus, 5.5, 0.77, 1.3);
   if (rows_us <= us256 && rows_us <= us128) return 0;
   return us256 <= us128 ? 1 : 2;
@@ -650,8 +655,9 @@ static hipError_t launch(const Mxfp4GemmArgs& g, int variant, hipStream_t s) {
   // up to 16 rows a group: half the registers, twice the waves (32 groups of 7168 x 2048, 4 rows each: 43
   // against 55 us); above: 64 rows a pass (one group of 8192 x 8192, 64 rows: 16 against 27 us)
   if ((long long)g.rows <= 16LL * g.groups) {
-    // fewer workgroups than CUs: half the columns, eight waves along K (one row, 4099 x 7168: 5.6 against
-    // 7.3 us; one group of 8192 x 8192, which has enough: 12.2 against 10.0 us)
+    // fewer workgroups than CUs: half the columns, eight waves along K (one row, 4099 x 7168: 5.6 against 7.3 us;
+    // one group of 8192 x 8192, which has enough: 12.2 against 10.0 us).  Workgroups of groups without rows count:
+    // they take their time too (1 row in 256 groups of 1024 x 1024 10.4 against 5.0 us)
     if ((long long)g.groups * ((g.N + 31) / 32) < device_cus()) return launch_rows<T, 8, 1, 32>(g, s);
     return launch_rows<T, 4, 2, 32>(g, s);
   }

@@ -305,6 +305,31 @@ def test_plain_product_without_offsets(rows, variant):
     assert torch.equal(p.run((a, asf, b, bsf, None)).double(), p.ref())
 
 
+def random_product(rows, N, K, G, sizes, seed):
+    """Codes, scales over 2^-11 .. 2^0 and offsets, made on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    byte = lambda lo, hi, *n: torch.randint(lo, hi, n, dtype=torch.uint8, device="cuda", generator=g)  # noqa: E731
+    words = lambda m: byte(116, 128, (K + 127) // 128, (m + 3) // 4 * 4, 4).view(torch.int32)  # noqa: E731
+    off = torch.from_numpy(np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)).cuda()
+    return byte(0, 256, rows, K // 2), words(rows), byte(0, 256, G, N, K // 2), words(G * N), off
+
+
+def product_of(args, rows, N, K, G, variant):
+    c = torch.full((rows, N), 77.0, device="cuda")
+    B.moe_mxfp4_gemm(B.make_mxfp4_gemm_desc(rows, N, K, G, "f32", variant=variant), *args, c)
+    return c
+
+
+@pytest.mark.parametrize("rows,G,N,K", [(1, 32, 4096, 7168), (8, 64, 4096, 7168), (4, 256, 512, 4096)])
+def test_choice_of_kernel_with_fewer_rows_than_groups(rows, G, N, K):
+    """Only the groups that have rows are read: the choice is the rows kernel's, by which the sum along K is split
+    over waves.  Float32 results tell it from the tiles, which sum in one run."""
+    sizes = np.bincount(np.random.RandomState(rows).permutation(G)[:rows], minlength=G)
+    args = random_product(rows, N, K, G, sizes, 1)
+    auto, by_rows, by_tiles = (product_of(args, rows, N, K, G, v) for v in (-1, 0, 2))
+    assert torch.equal(auto, by_rows) and not torch.equal(auto, by_tiles)
+
+
 @pytest.mark.parametrize("variant", [0, 1, 2])
 def test_product_many_groups(variant):
     """1024 groups, most of them empty: the tile plan's largest size."""
