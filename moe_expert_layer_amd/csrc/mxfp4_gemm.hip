@@ -187,6 +187,9 @@ struct TileCfg {
   static constexpr int kScales = 2 * kSlot;          // four slots of [word][A's rows], [word][B's rows]
   static constexpr int kScaleSlot = (BM + BN) * 8;
   static constexpr int kPlan = kScales + 4 * kScaleSlot;
+  static constexpr int lds_bytes(int groups) { return kPlan + (3 * groups + 1 + NW) * 4; }
+  // workgroups that a CU's LDS holds: of the 128 x 128 tiles' two with up to 681 groups, one with more
+  static constexpr int per_cu(int groups) { return 160 * 1024 / lds_bytes(groups); }
   static constexpr int kADma = BM / 8 / NW, kBDma = BN / 8 / NW;  // 1 KB loads per wave and stage
   static constexpr int kSDma = (BM + BN) * 2 / 64 / NW;           // 256-byte loads of scale words
   static constexpr int kPer = kADma + kBDma + kSDma;              // loads per wave and stage
@@ -194,6 +197,9 @@ struct TileCfg {
   static_assert(kSDma * NW * 32 == BM + BN && BM % 64 == 0 && BN % 64 == 0, "");
   static_assert(NW * 32 * 256 <= kSlot && WTN == 128, "the results' staging fits a slot, in passes of 256 bytes");
 };
+
+using Tiles256 = TileCfg<256, 256, 8, 64, 128>;
+using Tiles128 = TileCfg<128, 128, 4, 32, 128>;
 
 template <typename T, int BM, int BN, int NW, int WTM, int WTN>
 __global__ __launch_bounds__(NW * 64, 1) void mxfp4_gemm_tile_kernel(Mxfp4GemmArgs g) {
@@ -578,24 +584,21 @@ static hipError_t launch_tiles(const Mxfp4GemmArgs& g, hipStream_t s) {
   using C = TileCfg<BM, BN, NW, WTM, WTN>;
   auto kern = mxfp4_gemm_tile_kernel<T, BM, BN, NW, WTM, WTN>;
   constexpr int kMaxGroups = 1024;
-  const size_t bytes = C::kPlan + (size_t)(3 * g.groups + 1 + NW) * 4;
   static std::atomic<uint64_t> ready{0};  // the LDS limit is raised once per device
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
-    e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize,
-                            C::kPlan + (3 * kMaxGroups + 1 + NW) * 4);
+    e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, C::lds_bytes(kMaxGroups));
     if (e != hipSuccess) return e;
     ready.fetch_or(bit, std::memory_order_acq_rel);
   }
-  // at most this many tiles; as many workgroups as the LDS lets a CU hold (with up to some 600 groups), in whole
-  // rows of 8 XCDs
+  // at most this many tiles; as many workgroups as fit the GPU at once, in whole rows of 8 XCDs
   const long long most = (((long long)g.rows + (long long)g.groups * (BM - 1)) / BM) * ((g.N + BN - 1) / BN);
-  const long long room = (long long)device_cus() * (160 * 1024 / (C::kPlan + 8 * 1024));
+  const long long room = (long long)device_cus() * C::per_cu(g.groups);
   const unsigned grid = (unsigned)(((most < room ? most : room) + 7) / 8 * 8);
-  kern<<<dim3(grid), dim3(C::NT), bytes, s>>>(g);
+  kern<<<dim3(grid), dim3(C::NT), C::lds_bytes(g.groups), s>>>(g);
   return hipGetLastError();
 }
 
@@ -620,10 +623,12 @@ static hipError_t launch_rows(const Mxfp4GemmArgs& g, hipStream_t s) {
 // its workgroups without rows take to come and go, 0.25 us a thousand (1 row in 256 groups of 7168 x 2048: 18 us,
 // with 128 x 128 tiles 11; in 32 groups of 4096 x 7168 9.6 and 21 us).  The figures are fitted to 501 shapes (1 to 32
 // groups of 1 to 2048 rows, nine N x K from 300 x 64 to 8192 x 8192), where the choice is on average 0.2% off the
-// fastest, as it is on 166 with fewer rows than groups (2 to 1024 of them), spread over the groups.  Measured, rows /
-// 256 / 128: one group of 8192 x 8192: 64 rows 15 / 44 / 24 us, 200 rows 42 / 46 / 25 us; 8 groups of 4096 x 4096: 64
-// rows each 35 / 26 / 16 us; 32 groups of 4096 x 7168: 4 rows each 93 / 96 / 85 us, 32 rows 133 / 102 / 89 us, 128 rows
-// 366 / 119 / 130 us; 8192 x 8192 x 8192 - / 265 / 344 us.
+// fastest, as it is on 166 with fewer rows than groups (2 to 1024 of them), spread over the groups; it is 1% off on 60
+// with 720 and 1024 groups, where one workgroup of the 128 x 128 tiles fits a CU (4 rows each in 720 groups of
+// 512 x 4096: 142 / 167 / 203 us; 16 of 2048 x 2048: 355 / 371 / 437), and 3.5% on 60 with 256 and 640.  Measured,
+// rows / 256 / 128: one group of 8192 x 8192: 64 rows 15 / 44 / 24 us, 200 rows 42 / 46 / 25 us; 8 groups of
+// 4096 x 4096: 64 rows each 35 / 26 / 16 us; 32 groups of 4096 x 7168: 4 rows each 93 / 96 / 85 us, 32 rows
+// 133 / 102 / 89 us, 128 rows 366 / 119 / 130 us; 8192 x 8192 x 8192 - / 265 / 344 us.
 static int choose(const Mxfp4GemmArgs& g) {
   const int active = g.rows < g.groups ? g.rows : g.groups;  // groups that can have rows
   const double avg = (double)((g.rows + active - 1) / active), cus = device_cus(), stages = (g.K + 255) / 256;
@@ -639,7 +644,8 @@ static int choose(const Mxfp4GemmArgs& g) {
   const double base_us = empty_us > fixed_us ? empty_us : fixed_us;
   const double rows_us = (weights_us > base_us ? weights_us : base_us) +
                          2.7e-9 * (avg <= 16 ? avg : (double)(((int)avg + 15) / 16 * 16)) * active * g.N * g.K;
-  const double us256 = tiles_us(256, cus, 7.1, 0.98, 1.7), us128 = tiles_us(128, 2 * cus, 5.5, 0.77, 1.3);
+  const double us256 = tiles_us(256, cus * Tiles256::per_cu(g.groups), 7.1, 0.98, 1.7);
+  const double us128 = tiles_us(128, cus * Tiles128::per_cu(g.groups), 5.5, 0.77, 1.3);
   if (rows_us <= us256 && rows_us <= us128) return 0;
   return us256 <= us128 ? 1 : 2;
 }

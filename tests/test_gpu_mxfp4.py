@@ -330,6 +330,23 @@ def test_choice_of_kernel_with_fewer_rows_than_groups(rows, G, N, K):
     assert torch.equal(auto, by_rows) and not torch.equal(auto, by_tiles)
 
 
+def test_choice_of_kernel_with_many_groups():
+    """From 682 groups on the LDS of a CU holds one workgroup of the 128 x 128 tiles instead of two, and the choice is
+    the rows kernel's (told by its float32 results)."""
+    rows, G, N, K = 2880, 720, 512, 4096
+    args = random_product(rows, N, K, G, np.full(G, 4), 2)
+    auto, by_rows, by_tiles = (product_of(args, rows, N, K, G, v) for v in (-1, 0, 2))
+    assert torch.equal(auto, by_rows) and not torch.equal(auto, by_tiles)
+
+
+@pytest.mark.parametrize("variant", [1, 2])
+@pytest.mark.parametrize("G", [681, 682, 1024])
+def test_product_more_tiles_than_workgroups_of_many_groups(G, variant):
+    r = np.random.RandomState(G)
+    p = Product(list(r.randint(0, 7, G)), 130, 288, rows=6 * G, seed=G, variant=variant)
+    assert torch.equal(p.run().double(), p.ref())
+
+
 @pytest.mark.parametrize("variant", [0, 1, 2])
 def test_product_many_groups(variant):
     """1024 groups, most of them empty: the tile plan's largest size."""
