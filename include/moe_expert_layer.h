@@ -331,7 +331,7 @@ moe_status moe_unpack_scales(int32_t rows, int32_t groups, const int32_t* packed
  *   - Rows that no slot owns, and the elements between H and the stride, are left as they were.
  *   - slot_to_row comes from moe_sort_tokens or moe_route_permute; a map entry outside
  *     [0, max_rows) counts as no row, so rows past the caller's tensors are dropped.  Two slots
- *     with one row (not something the sort makes) give that row from either.
+ *     with one row (not something the sort makes) give each element of that row from either.
  *   - Pointers are aligned to their element; outputs must not overlap inputs or each other.
  *     Stream, validation and error rules are those at the top of this file.  num_tokens = 0
  *     launches nothing.
@@ -360,7 +360,9 @@ moe_status moe_sort_workspace_size(const moe_dispatch_desc* desc, size_t* bytes)
 /* Group the (token, slot) pairs by local expert, stable by slot id, from expert ids of any
  * router: counts, offsets, row_to_slot and slot_to_row as moe_route_permute writes them (same
  * sizes and meaning).  An id outside the local experts, negative ones among them, is not local.
- * hidden, dtype, max_rows and the strides are not used (they must be valid). */
+ * hidden, dtype, max_rows and the strides are not used (they must be valid): counts, offsets and
+ * both maps are those of all local slots, also where these are more than max_rows.  With
+ * num_tokens = 0 counts and offsets are not written either. */
 moe_status moe_sort_tokens(const moe_dispatch_desc* desc, const int32_t* topk_ids, int32_t* counts, int32_t* offsets,
                            int32_t* row_to_slot, int32_t* slot_to_row, void* workspace, size_t workspace_bytes,
                            void* stream);
@@ -435,12 +437,15 @@ typedef struct {
  *   c[r, n] = sum_k a[r, k] * b[e, n, k]   for offsets[e] <= r < offsets[e + 1]
  * a [rows, K] (say, quantised tokens in expert order), b [groups, N, K], offsets int32
  * [groups + 1] on the device, ascending from 0 (moe_sort_tokens), or NULL with one group: all rows
- * (a plain product).  Rows of c at or past offsets[groups] are left as they were.  Offsets outside
- * [0, rows] or descending give unspecified results, but no access outside the tensors.  The sum's
- * order depends on the sizes only, so results are the same from run to run.  a and b 16-byte
- * aligned, scales 4-byte, c to its element; c must not overlap the inputs.  No workspace.  Scale
- * byte 255 makes every result that reads it NaN.  Errors as for the other calls; MOE_ERR_UNSUPPORTED for
- * row-major scales with K not a multiple of 128 (moe_pack_scales packs them). */
+ * (a plain product).  Ascending offsets are cut to [0, rows]: with the offsets of a sort that found
+ * more rows than the caller's tensors hold, the rows that are there are computed and the others
+ * dropped, as moe_dispatch and moe_combine drop them with max_rows = rows.  Rows of c in no group
+ * are left as they were.  Descending offsets give unspecified results, but no access outside the
+ * tensors.  The sum's order depends on the sizes only, so results are the same from run to run.
+ * a and b 16-byte aligned, scales 4-byte, c to its element; c must not overlap the inputs.  No
+ * workspace.  Scale byte 255 makes every result that reads it NaN.  Errors as for the other calls;
+ * MOE_ERR_UNSUPPORTED for row-major scales with K not a multiple of 128 (moe_pack_scales packs
+ * them). */
 moe_status moe_mxfp4_gemm(const moe_mxfp4_gemm_desc* desc, const uint8_t* a, const void* a_sf, const uint8_t* b,
                           const void* b_sf, const int32_t* offsets, void* c, void* stream);
 

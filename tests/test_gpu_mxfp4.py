@@ -297,6 +297,57 @@ def test_product_offsets_are_cut_to_the_rows(rows, variant):
     assert torch.equal(c.cpu().double(), torch.from_numpy(av @ bv[0].T))
 
 
+def guarded(rows, ld, n, guard=300):
+    """c [rows, n] of float32, its rows ld apart, with more than a tile's rows before and behind it, all 77; and what
+    the rows around c and the padding of its own hold after a call."""
+    buf = torch.full((rows + 2 * guard, ld), 77.0, device="cuda")
+
+    def rest():
+        b = buf.cpu()
+        return torch.cat([b[:guard].reshape(-1), b[guard + rows:].reshape(-1), b[:, n:].reshape(-1)])
+
+    return buf[guard:guard + rows, :n], rest
+
+
+@pytest.mark.parametrize("variant", [-1, 0, 1, 2])
+@pytest.mark.parametrize("K", [256, 1056])
+@pytest.mark.parametrize("rows,off", [
+    (250, [0, 130, 130, 200, 500, 520]),     # a group across the last row, one behind it
+    (20, [0, 3, 19, 20, 21, 4000]),          # small groups, the last row's group ends with it
+    (600, [0, 0, 1, 601, 601, 2 ** 31 - 1]),
+    (300, [290, 295, 299, 300, 310, 310]),   # rows before the first group
+    (300, [-400, -7, 5, 290, 300, 301]), (40, [40, 50, 60, 70, 80, 90]), (40, [-9, -8, -7, -6, 0, 0])])
+def test_product_ascending_offsets_are_cut(rows, off, K, variant):
+    """Ascending offsets reach past the tensors' rows (a sort that found more rows than there is room for) or start
+    elsewhere: every row inside is its group's product, the others and everything around c stay as they were."""
+    G, N = len(off) - 1, 48
+    p = Product([rows] + [0] * (G - 1), N, K, seed=rows, variant=variant)
+    a, asf, b, bsf, _ = p.args()
+    desc = B.make_mxfp4_gemm_desc(rows, N, K, G, "f32", variant=variant, out_stride=N + 3)
+    c, rest = guarded(rows, N + 3, N)
+    B.moe_mxfp4_gemm(desc, a, asf, b, bsf, torch.tensor(off, dtype=torch.int32, device="cuda"), c)
+    av, bv = values_ref(p.ac, p.ab), values_ref(p.bc, p.bb).reshape(G, N, K)
+    want = np.full((rows, N), 77.0)
+    for e in range(G):
+        lo, hi = (min(max(o, 0), rows) for o in off[e:e + 2])
+        want[lo:hi] = av[lo:hi] @ bv[e].T
+    assert torch.equal(c.cpu().double(), torch.from_numpy(want))
+    assert (rest() == 77).all()
+
+
+@pytest.mark.parametrize("variant", [0, 1, 2])
+@pytest.mark.parametrize("rows", [20, 300, 700])
+def test_product_descending_offsets_stay_inside_the_tensors(rows, variant):
+    """Groups that overlap or end before they start: the results are anyone's, but nothing around c is written."""
+    p = Product([rows, 0, 0], 48, 256, seed=1, variant=variant)
+    a, asf, b, bsf, _ = p.args()
+    desc = B.make_mxfp4_gemm_desc(rows, 48, 256, 3, "f32", variant=variant, out_stride=50)
+    for off in ([-5, rows // 2, 3, 2 * rows], [0, 1 << 30, 5, -7], [rows, 0, rows, 0], [5, 0, rows + 9, 2]):
+        c, rest = guarded(rows, 50, 48)
+        B.moe_mxfp4_gemm(desc, a, asf, b, bsf, torch.tensor(off, dtype=torch.int32, device="cuda"), c)
+        assert (rest() == 77).all()
+
+
 @pytest.mark.parametrize("variant", [0, 1, 2])
 @pytest.mark.parametrize("rows", [3, 300])
 def test_plain_product_without_offsets(rows, variant):
@@ -513,3 +564,47 @@ def test_experts_from_their_parts():
     np.add.at(ref, rows, v)
     np.add.at(mag, rows, np.abs(v))
     assert (np.abs(y.double().cpu().numpy() - ref) <= np.abs(ref) * 2.0 ** -8 + (k + 2) * 2.0 ** -24 * mag + 1e-40).all()
+
+
+def test_rows_past_the_capacity_are_dropped_in_every_step():
+    """sort -> dispatch -> quantise -> product -> combine with tensors of fewer rows than the sort finds: the slots whose
+    rows are there give what float64 gives for them, the others nothing, and nothing past the rows is written."""
+    T, H, N, E, e0, el, k, cap = 120, 256, 96, 12, 2, 8, 4, 200
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()
+    top = torch.topk(torch.randn(T, E, generator=g).cuda(), k, dim=1)
+    ids, w = top.indices.to(torch.int32), torch.softmax(top.values, 1)
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    counts, off, r2s, s2r = i32(el), i32(el + 1), i32(T * k), i32(T * k)
+    d = B.make_dispatch_desc(T, H, E, k, local_begin=e0, num_local=el, max_rows=cap)
+    B.moe_sort_tokens(d, ids, counts, off, r2s, s2r, B.alloc_sort_workspace(d))
+    o = off.cpu().numpy()
+    cut = np.minimum(o, cap)
+    straddled = int(np.searchsorted(o, cap, side="left")) - 1
+    assert o[-1] > cap + 50 and o[straddled] < cap < o[straddled + 1] and straddled < el - 1
+    xs = torch.full((cap + 300, H), 77.0, dtype=torch.bfloat16, device="cuda")
+    B.moe_dispatch(d, x, s2r, xs[:cap])
+    tok = r2s.cpu().numpy()[:cap] // k
+    assert torch.equal(xs.cpu()[:cap], x.cpu()[tok]) and (xs[cap:] == 77).all()
+    a = torch.zeros(cap, H // 2, dtype=torch.uint8, device="cuda")
+    asf = torch.zeros(H // 128, cap, dtype=torch.int32, device="cuda")
+    B.moe_quantize_mxfp4(B.make_mxfp4_desc(cap, H, scale_layout="packed"), xs[:cap], a, asf)
+    av = values_ref(*quantize_ref(x.double().cpu().numpy()[tok]))
+    bc, bb = np.random.RandomState(1).randint(0, 16, (el * N, H)).astype(np.uint8), np.full((el * N, H // 32), 122, np.uint8)
+    bv = values_ref(bc, bb).reshape(el, N, H)
+    ys, rest = guarded(cap, N, N)
+    B.moe_mxfp4_gemm(B.make_mxfp4_gemm_desc(cap, N, H, el, "f32"), a, asf, torch.from_numpy(nibbles(bc)).cuda(),
+                     scales_dev(bb, "packed"), off, ys)
+    assert (rest() == 77).all()
+    ref, mag = (np.concatenate([f(av[cut[e]:cut[e + 1]]) @ f(bv[e]).T for e in range(el)]) for f in (np.array, np.abs))
+    # H / 64 matrix instructions round the running sum, up to 16 partial sums are added
+    assert (np.abs(ys.double().cpu().numpy() - ref) <= (H / 64 + 17) * 2.0 ** -23 * mag).all()
+    y = torch.full((T, N), 77.0, device="cuda")
+    dn = B.make_dispatch_desc(T, N, E, k, local_begin=e0, num_local=el, dtype="f32", max_rows=cap)
+    B.moe_combine(dn, ys, s2r, w, y)
+    v = ys.double().cpu().numpy() * w.double().cpu().reshape(-1).numpy()[r2s.cpu().numpy()[:cap]][:, None]
+    want, size = np.zeros((T, N)), np.zeros((T, N))
+    np.add.at(want, tok, v)
+    np.add.at(size, tok, np.abs(v))
+    assert (np.abs(y.double().cpu().numpy() - want) <= (k + 2) * 2.0 ** -24 * size).all()
+    assert (y.cpu()[torch.from_numpy(~np.isin(np.arange(T), tok))] == 0).all()
