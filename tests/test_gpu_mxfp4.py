@@ -164,6 +164,29 @@ def test_quantized_weights_run_the_layer():
     assert G.rel_fro(G.bf16_to_f64(got["y_bf16"]), G.bf16_to_f64(ref["y_bf16"])) <= 2e-3
 
 
+@pytest.mark.parametrize("layout", ["rows", "packed"])
+def test_quantize_offsets_past_32_bits(layout):
+    """Values of more than 2^32 elements (rows 2^16 + 1 elements apart) and codes of more than 2^31 bytes."""
+    M, K, pad = 65600, 1 << 16, 1
+    row = torch.randn(3, K, generator=torch.Generator().manual_seed(7)).to(torch.bfloat16)
+    code, byte = quantize_ref(row.double().numpy())
+    src = torch.zeros(M, K + pad, dtype=torch.bfloat16, device="cuda")[:, :K]
+    at = [0, 65000, M - 1]
+    src[at] = row.cuda()
+    codes = torch.full((M, K // 2), 77, dtype=torch.uint8, device="cuda")
+    sf = (torch.full((K // 128, M), 77, dtype=torch.int32, device="cuda") if layout == "packed"
+          else torch.full((M, K // 32), 77, dtype=torch.uint8, device="cuda"))
+    d = B.make_mxfp4_desc(M, K, "bf16", layout, K + pad)
+    B.moe_quantize_mxfp4(d, src, codes, sf)
+    got = sf[:, at].t().contiguous().view(torch.uint8) if layout == "packed" else sf[at]
+    assert np.array_equal(codes[at].cpu().numpy(), nibbles(code)) and np.array_equal(got.cpu().numpy(), byte)
+    zero = [1, 40000, M - 2]
+    assert (codes[zero] == 0).all()
+    src.fill_(77.0)
+    B.moe_dequantize_mxfp4(d, codes, sf, src)
+    assert torch.equal(src[at].cpu().double(), torch.from_numpy(values_ref(code, byte))) and (src[zero] == 0).all()
+
+
 # ---- product ----
 
 class Product:
