@@ -32,9 +32,7 @@ __device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t ld
 // the same from a buffer: its base and length sit in a four-dword descriptor in SGPRs, soff is a
 // uniform byte offset, and a lane whose voff + soff reaches past the length reads nothing there (the
 // hardware checks every load: voff >= length - soff is out of range, so soff is kept within the
-// length).  The length is cut to 2^31 - 1, past which no caller's offsets reach; a voff of kNowhere is
-// then out of range in every buffer.
-constexpr uint32_t kNowhere = 0x80000000u;
+// length).  The length is cut to 2^31 - 1, past which no caller's offsets reach.
 typedef int v4i_srd __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ v4i_srd buffer_srd(const void* base, long long bytes) {
   const uint64_t b = reinterpret_cast<uint64_t>(base);
