@@ -36,7 +36,7 @@ PEAK_HBM_GBS = 8000.0      # MI355X HBM3E
 GRADED = ("mxfp4_large", "decode", "prefill_zipf")
 
 # the translation unit of the FC1 kernel: the HBM traffic counters stay valid while these are unchanged
-FC1_SOURCES = ("grouped_gemm.hip", "device_common.hpp", "moe_internal.hpp")
+FC1_SOURCES = ("grouped_gemm.hip", "device_common.hpp", "lds_dma.hpp", "moe_internal.hpp")
 
 
 def source_hash() -> str:

@@ -21,7 +21,7 @@
 
 #include "device_common.hpp"
 #include "elem.hpp"
-#include "moe_internal.hpp"
+#include "operators.hpp"
 
 namespace moe {
 

@@ -21,6 +21,7 @@
 
 #include "../../include/moe_expert_layer.h"
 #include "moe_internal.hpp"
+#include "operators.hpp"
 
 namespace {
 

@@ -18,6 +18,7 @@
 #include "elem.hpp"
 #include "lds_dma.hpp"
 #include "moe_internal.hpp"
+#include "operators.hpp"
 
 namespace moe {
 

@@ -20,7 +20,7 @@
 
 #include "device_common.hpp"
 #include "elem.hpp"
-#include "moe_internal.hpp"
+#include "operators.hpp"
 
 namespace moe {
 
