@@ -35,8 +35,8 @@ __device__ __forceinline__ uint64_t token_rows(const int32_t* __restrict__ s2r, 
 
 // grid (column chunks, tokens): 256 threads on 1, 2 or 4 tokens, PER 16-byte chunks of a row each, read once
 // and stored to every row the token has (a kernel by rows would read a token up to k times).  128 tokens of
-// 14 KB, 125 rows: 2.5 us, the latency of map -> row -> store; 4096 tokens, 4136 rows: 16 us, 7.3 TB/s from the
-// caches; 32768 tokens, 32586 rows: 151 us, 6.2 TB/s.
+// 14 KB, 125 rows: 2.5 to 3 us, the latency of map -> row -> store; 4096 tokens, 4136 rows: 16 us, 7.3 TB/s from the
+// caches, 30900 rows: 98 us, 5.1 TB/s; 32768 tokens, 32600 rows of 21600 of them: 152 us, 5.1 TB/s.
 template <int PER>
 __global__ __launch_bounds__(256) void dispatch_kernel(const uint8_t* __restrict__ x, long long x_pitch,
                                                        const int32_t* __restrict__ s2r, int T, int k, int max_rows,
@@ -77,8 +77,8 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const uint8_t* __restrict
 // y[t] = sum over the token's rows of weight * row (WEIGHTED) or of the rows themselves.
 // grid (column chunks, tokens): 256 threads on 1, 2 or 4 tokens, one 16-byte chunk each; the rows are taken four at a
 // time, their loads issued before the sum.  32768 tokens of 7168 bfloat16 values with 32700 rows:
-// 193 us, 4.9 TB/s, what a copy of 2 GiB reaches; 4097 tokens of 2050 float32 values, 4 rows each:
-// 34 us, 4.9 TB/s; one token: 3.0 us.
+// 193 to 200 us, 4.7 to 4.9 TB/s, what a copy of 2 GiB reaches; 4097 tokens of 2050 float32 values, 4 rows each:
+// 34 us, 4.9 TB/s; one token: 3.0 to 3.3 us.
 template <typename T, bool WEIGHTED>
 __global__ __launch_bounds__(256) void combine_rows_kernel(const T* __restrict__ ys, long long ys_stride,
                                                            const int32_t* __restrict__ s2r,
@@ -156,7 +156,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 // split into n parts of P = NW / n: each part takes one row, each of its waves every P-th 64-chunk piece
 // of it, so the work is spread whether a token has one local row or all k of them.  (n > NW: the waves
 // take the rows in turn.)  dy is read by every part, from the L1 after the first.  16384 tokens of 4096 bfloat16 values, 8 rows each:
-// 461 us, 5.0 TB/s, what a copy reaches; 512 tokens of 2048 float16 values, 4 rows each: 6.6 us.
+// 454 to 461 us, 5.0 TB/s, what a copy reaches; 512 tokens of 2048 float16 values, 4 rows each: 6.6 us.
 template <typename T, int NW, int G>
 __global__ __launch_bounds__(NW * G * 64) void combine_backward_kernel(
     const T* __restrict__ dy, long long dy_stride, const T* __restrict__ ys, long long row_stride,

@@ -38,10 +38,11 @@ __device__ __forceinline__ v8i fp4_operand(uint4 q) {
 // the matrix instruction's registers (a weight is used once per 16 rows: nothing to gain from LDS), and
 // their partial sums meet in LDS, in wave order.  Rows go 16, 32 or 64 at a time (MT); a group with
 // more is walked again, or by other workgroups (the grid's z).  Bound by HBM: 4 rows for each of 32
-// groups of 4096 x 7168 take 90 us, 5.5 TB/s of weights (5.6 by the layer's own decode FC1).
+// groups of 4096 x 7168 take 89 us, 5.6 TB/s of weights, as the layer's own decode FC1 reads them (93 to 96 us a
+// call in a captured graph).
 template <typename T, int NW, int NS, int MAXR, int MT>
-__device__ __forceinline__ void gemm_rows(const Mxfp4GemmArgs& g, float (*part)[MAXR][NS * 16 + 1], int e, int n0, int m0,
-                                          int m_end) {
+__device__ __forceinline__ void gemm_rows(const Mxfp4GemmArgs& g, float (*part)[MAXR][NS * 16 + 1], int e, int n0,
+                                          int m0, int m_end) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r16 = lane & 15, q = lane >> 4;
   const int nblk = g.K / 32, nwords = (nblk + 3) / 4, nst = (nwords + 3) / 4;
@@ -163,11 +164,13 @@ __global__ __launch_bounds__(NW * 64) void mxfp4_gemm_rows_kernel(Mxfp4GemmArgs 
 // are persistent: each XCD has a contiguous range of tiles, whose rows and columns of operands meet in
 // its L2, and its workgroups take them in turn.
 //
-// Measured: 32500 rows x 4096 x 7168 in 32 groups 510 to 540 us, 3.5 to 3.7 PFLOP/s; 8192 x 8192 x 8192
-// 260 us, 4.2; 4096 x 4096 x 57344, where the K loop is all there is, 410 to 430 us, 4.5 to 4.65.  What
-// bounds the K loop is power: it keeps the matrix cores busy 60 to 64% of its cycles at 1.75 to 1.8 GHz
-// (2.4 GHz when it has nothing to multiply), and a version that was busy 51% of them ran at 2.0 GHz and
-// hardly slower.  A tile's results cost 7 us, all workgroups storing at once.  Not kept: 128 x 128 per
+// Measured: 32500 rows x 4096 x 7168 in 32 groups 500 to 570 us by box and clock, 3.3 to 3.8 PFLOP/s; 8192 x 8192 x
+// 8192 260 us, 4.2; 4096 x 4096 x 57344, where the K loop is all there is, 410 to 430 us, 4.5 to 4.65.  On the last
+// the matrix cores are busy 60 to 64% of the cycles at 1.75 to 1.8 GHz (2.4 GHz with nothing to multiply), so that
+// half of every cycle saved is lost to the power limit (897K cycles 452 us, 727K 409 us).  On the first they are busy
+// 47% of the cycles, at 1.9 to 2.0 GHz, and 34% of the L2's requests miss: about 12 of the 32 groups end with a tile
+// of a few rows, which costs about as much as a full one (32 groups of 1024 rows 500 us, of 1030 rows 578 us), and a
+// tile's results cost 7 us, all workgroups storing at once.  Not kept: 128 x 128 per
 // wave, four waves (656 us on the last shape: one wave a SIMD waits for its own loads to issue); half-line
 // stages, four of them (472 us, twice the L2 requests); results stored from the registers, 32 bytes a row
 // at a time (680 against 525 us on the first shape); lines of later stages touched ahead, by every wave
@@ -607,7 +610,7 @@ template <typename T, int NW, int NS, int MAXR>
 static hipError_t launch_rows(const Mxfp4GemmArgs& g, hipStream_t s) {
   const unsigned x = (unsigned)((g.N + 16 * NS - 1) / (16 * NS)), y = (unsigned)g.groups;
   // few columns: the passes over rows spread over the grid up to 4096 waves, 16 per CU (one group may have all the
-  // rows).  5826 rows x 32 x 4768 in 7 groups 87 -> 9 us, 334 rows x 1744 x 6592 37 -> 14; with half the waves
+  // rows).  5826 rows x 32 x 4768 in 7 groups 87 -> 8 us, 334 rows x 1744 x 6592 37 -> 18; with half the waves
   // 1197 rows x 508 x 1728 in 7 groups 8.2 instead of 6.6 us, with twice as many 6.9.
   const long long room = 4096 / NW / ((long long)x * y), most = (g.rows + MAXR - 1) / MAXR;
   const unsigned z = (unsigned)(room < 1 ? 1 : room < most ? room : most);
@@ -623,13 +626,15 @@ static hipError_t launch_rows(const Mxfp4GemmArgs& g, hipStream_t s) {
 // are fewer rows than groups, only as many groups as rows count, and the rows kernel needs at least the time that
 // its workgroups without rows take to come and go, 0.25 us a thousand (1 row in 256 groups of 7168 x 2048: 18 us,
 // with 128 x 128 tiles 11; in 32 groups of 4096 x 7168 9.6 and 21 us).  The figures are fitted to 501 shapes (1 to 32
-// groups of 1 to 2048 rows, nine N x K from 300 x 64 to 8192 x 8192), where the choice is on average 0.2% off the
-// fastest, as it is on 166 with fewer rows than groups (2 to 1024 of them), spread over the groups; it is 1% off on 60
-// with 720 and 1024 groups, where one workgroup of the 128 x 128 tiles fits a CU (4 rows each in 720 groups of
-// 512 x 4096: 142 / 167 / 203 us; 16 of 2048 x 2048: 355 / 371 / 437), and 3.5% on 60 with 256 and 640.  Measured,
-// rows / 256 / 128: one group of 8192 x 8192: 64 rows 15 / 44 / 24 us, 200 rows 42 / 46 / 25 us; 8 groups of
-// 4096 x 4096: 64 rows each 35 / 26 / 16 us; 32 groups of 4096 x 7168: 4 rows each 93 / 96 / 85 us, 32 rows
-// 133 / 102 / 89 us, 128 rows 366 / 119 / 130 us; 8192 x 8192 x 8192 - / 265 / 344 us.
+// groups of 1 to 2048 rows, all alike, nine N x K from 300 x 64 to 8192 x 8192), where the choice is on average 0.2%
+// off the fastest; on 170 with fewer rows than groups (2 to 1024 of them) it is 0.1% off, on 60 with 720 and 1024 groups,
+// where one workgroup of the 128 x 128 tiles fits a CU, 1% (4 rows each in 720 groups of 512 x 4096: 142 / 167 / 203
+// us), on 90 with 64 to 640 groups 2.8%.  Groups of very different sizes, which the host does not see, cost more:
+// Zipf shares 3.6% up to 32 groups, 15 to 20% from 64 on, most where K is short and a few groups have many rows
+// (25600 in 640 groups of 256 x 512: 127 / 27 / 21 us).  Measured, rows / 256 / 128: one group of 8192 x 8192: 64 rows
+// 15 / 44 / 24 us, 200 rows 42 / 46 / 25 us; 8 groups of 4096 x 4096: 64 rows each 35 / 26 / 16 us; 32 groups of
+// 4096 x 7168: 4 rows each 93 / 96 / 85 us, 32 rows 133 / 102 / 89 us, 128 rows 366 / 119 / 130 us; 8192 x 8192 x 8192
+// - / 265 / 344 us.
 static int choose(const Mxfp4GemmArgs& g) {
   const int active = g.rows < g.groups ? g.rows : g.groups;  // groups that can have rows
   const double avg = (double)((g.rows + active - 1) / active), cus = device_cus(), stages = (g.K + 255) / 256;

@@ -12,9 +12,9 @@
 // columns of 8 rows; a lane 8 values of a row (one or two 16-byte loads), so 4 lanes hold a block
 // and its amax is a two-step DPP maximum.  The scale bytes of the tile meet in LDS and leave as
 // runs in either layout: words of 8 consecutive rows (packed int32 MN-major), or 16 bytes of a row.
-// Measured: 16384 x 7168 float32 quantised in 106 us (5.0 TB/s; 128 us with 32-row tiles, whose packed
+// Measured: 16384 x 7168 float32 quantised in 101 to 107 us (5.0 TB/s; 128 us with 32-row tiles, whose packed
 // words fill whole lines but whose waves are half as many; 116 us without the non-temporal loads),
-// values back as bfloat16 in 51 us (5.8 TB/s); 129 x 7168 bfloat16: 3.3 us and 3.4 us.
+// values back as bfloat16 in 50 to 51 us (5.8 TB/s); 129 x 7168 bfloat16: 3.4 us each.
 #include <hip/hip_runtime.h>
 #include <cstdint>
 
