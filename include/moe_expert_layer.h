@@ -12,8 +12,9 @@
  *   combine  top-k weighted sum back into token order (no atomics, fixed slot order)
  *
  * Beside the layer (at the end of this file): its parts for callers with a router or experts of
- * their own (tokens sorted by expert and back, with gradients), and MXFP4 quantisation and
- * grouped products.
+ * their own (tokens sorted by expert and back, with gradients), MXFP4 quantisation and
+ * grouped products, the router's balance loss with its gradient, and 4-bit weights with group
+ * scales for 16-bit rows.
  *
  * Sources: the fused "Mega MoE" expert layer as described by DeepGEMM PR #445
  * ("fix(sm90): support parameterized SwiGLU in FP8 MegaMoE": Summary, Changes,
@@ -448,6 +449,152 @@ typedef struct {
  * them). */
 moe_status moe_mxfp4_gemm(const moe_mxfp4_gemm_desc* desc, const uint8_t* a, const void* a_sf, const uint8_t* b,
                           const void* b_sf, const int32_t* offsets, void* c, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * The router's balance loss: per-expert counts, the loss, and the routing logits' gradient.
+ *
+ * The tokens lie in sequences: sequence s holds the tokens t with seq_offsets[s] <= t <
+ * seq_offsets[s + 1] whose mask byte is not 0 (no mask: all of them), N_s in number.  Tokens in no
+ * sequence or with mask 0 are padding: they add nothing, whatever their logits and ids hold.
+ *   p[t, e]         = softmax of logits[t] (MOE_SCORE_SOFTMAX), or sigmoid(logits[t, e]) over the
+ *                     sum of the token's sigmoids (MOE_SCORE_SIGMOID)
+ *   counts[s, e]    = the number of (t, j) in sequence s with topk_ids[t, j] = e
+ *   tokens[s]       = N_s
+ *   prob_sums[s, e] = sum over the tokens of s of p[t, e]
+ *   balance[s]      = E_tot / (k N_s^2) * sum_e counts[s, e] * prob_sums[s, e]
+ *                     (E_tot times the sum of share chosen times mean probability; 1 when even)
+ *   z[s]            = 1 / N_s * sum over the tokens of s of (log sum_e exp logits[t, e])^2
+ *   dlogits[t, e]   = add[t, e] + dbalance[s] * E_tot / (k N_s^2) * p[t, e] * q[t, e] *
+ *                       (counts[s, e] - sum_i p[t, i] * counts[s, i])
+ *                     + dz[s] * 2 / N_s * p[t, e] * log sum_i exp logits[t, i]
+ *                     with q = 1 (softmax) or 1 - sigmoid(logits[t, e]); padding tokens: add[t, e]
+ * The counts are not differentiated.  The backward call takes counts and tokens as the forward call
+ * wrote them, or sums of them over several GPUs' parts of a batch, which gives the gradient of the
+ * loss of the whole batch (the sums of its counts and of its probabilities).
+ *
+ *   - logits [T, E_tot] in the descriptor's dtype, rows logit_stride elements apart; dlogits and add
+ *     float32, rows grad_stride apart.  topk_ids int32 [T, k] of any router; an id outside
+ *     [0, E_tot) is not counted.  mask uint8 [T] or NULL.  seq_offsets int32 [num_seqs + 1] on the
+ *     device, ascending, cut to [0, T]; NULL with one sequence: all tokens.  Descending offsets give
+ *     unspecified results, but no access outside the tensors.
+ *   - counts [num_seqs, E_tot] and tokens [num_seqs] int32, prob_sums [num_seqs, E_tot], balance, z,
+ *     dbalance and dz [num_seqs] float32, all dense.  A sequence without tokens has counts, sums and
+ *     losses of 0.
+ *   - A logit of -inf gives probability 0; a token whose logits are all -inf has probabilities 0,
+ *     adds 0 to z and has no gradient, but its ids are counted.  NaN (and, with softmax, +inf) makes
+ *     its token's probabilities and what they enter NaN.
+ *   - Probabilities are float32; sums over tokens run in a fixed order (no atomics in them), partial
+ *     sums in float32 over at most a few hundred tokens of one lane, the rest in float64; the counts' integer sums
+ *     do not depend on the order.  The same from run to run.
+ *   - Pointers are aligned to their element; add may be dlogits itself, otherwise outputs must not
+ *     overlap inputs or each other.  Stream, validation and error rules are those at the top of this file;
+ *     num_tokens = 0 launches nothing and writes nothing.
+ *   - Limits: 1 <= E_tot <= 1024; 1 <= k <= 16; 1 <= num_seqs <= 65536; T*k <= 2^31 - 2^17; strides 0
+ *     (= E_tot) or E_tot to 2^40. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+  int32_t num_tokens;    /* T >= 0 */
+  int32_t num_experts;   /* E_tot */
+  int32_t topk;          /* k */
+  int32_t num_seqs;      /* sequences */
+  int32_t dtype;         /* moe_dtype of the logits: bf16, f16 or f32 */
+  int32_t score;         /* moe_score */
+  int64_t logit_stride;  /* elements between rows of logits; 0 = E_tot */
+  int64_t grad_stride;   /* elements between rows of dlogits and add; 0 = E_tot */
+} moe_balance_desc;
+
+/* Bytes of workspace moe_balance_loss needs.  Host only; validates the descriptor. */
+moe_status moe_balance_workspace_size(const moe_balance_desc* desc, size_t* bytes);
+
+/* Counts, probability sums and losses.  opt_z NULL: no z (MOE_ERR_UNSUPPORTED when given with
+ * MOE_SCORE_SIGMOID).  The workspace is 256-byte aligned. */
+moe_status moe_balance_loss(const moe_balance_desc* desc, const void* logits, const int32_t* topk_ids,
+                            const uint8_t* opt_mask, const int32_t* opt_seq_offsets, int32_t* counts, int32_t* tokens,
+                            float* prob_sums, float* balance, float* opt_z, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Gradient of the routing logits.  opt_dz NULL: no z term (MOE_ERR_UNSUPPORTED when given with
+ * MOE_SCORE_SIGMOID); opt_add NULL: 0.  topk and the ids are those of counts.  Writes every row. */
+moe_status moe_balance_loss_backward(const moe_balance_desc* desc, const void* logits, const uint8_t* opt_mask,
+                                     const int32_t* opt_seq_offsets, const int32_t* counts, const int32_t* tokens,
+                                     const float* dbalance, const float* opt_dz, const float* opt_add, float* dlogits,
+                                     void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * 4-bit weights with group scales, and their product with 16-bit rows.
+ *
+ * INT4: a row of K weights is K/2 bytes of codes q in [0, 15] (element 2i in the low nibble of byte
+ * i), and for each group of G consecutive ones a scale s (bf16, f16 or f32) and, with zero points, a
+ * byte z: the weight is (q - z) * s, z = 8 without zero points.  Scales and zero points lie row-major
+ * [rows, K/G], dense.  Any zero byte is allowed. */
+typedef struct {
+  int32_t rows;         /* M, 0 to 2^30 */
+  int32_t k;            /* K, at most 2^20, a multiple of the group */
+  int32_t group;        /* G: 32, 64 or a multiple of 128 */
+  int32_t dtype;        /* moe_dtype of the values: bf16, f16 or f32 */
+  int32_t scale_dtype;  /* moe_dtype of the scales: bf16, f16 or f32 */
+  int32_t zeros;        /* 0: without zero points; 1: with */
+  int64_t stride;       /* elements between rows of the values; 0 = K */
+} moe_int4_desc;
+
+/* values [M, K] -> codes [M, K/2], scales and zero points [M, K/G].  With l the group's least value
+ * or 0, whichever is less, and h its largest or 0:
+ *   without zero points  s = max(-l, h) / 7,  q = clamp(round(v / s), -8, 7) + 8
+ *   with zero points     s = (h - l) / 15,    z = clamp(round(-l / s), 0, 15),
+ *                        q = clamp(round(v / s) + z, 0, 15)
+ * The quotient s is rounded to float32, then to the scales' type; the rounding to codes goes by the
+ * exact quotient by the rounded s, ties to even.  A group whose s is 0 (all zero, or s below the type)
+ * gets q = z = 0 with zero points and q = 8 without; one with a NaN or an infinity, or whose s is
+ * beyond the type, gets s = NaN and the same codes, and all its values read as NaN.  Deterministic
+ * and exact.  codes 16-byte aligned, the rest to their elements; zeros is NULL without zero points.
+ * Stream, validation and error rules are those at the top of this file; rows = 0 launches nothing. */
+moe_status moe_quantize_int4(const moe_int4_desc* desc, const void* values, uint8_t* codes, void* scales,
+                             uint8_t* zeros, void* stream);
+
+/* The inverse: values = (q - z) * s in float32, rounded to nearest even to desc->dtype. */
+moe_status moe_dequantize_int4(const moe_int4_desc* desc, const uint8_t* codes, const void* scales,
+                               const uint8_t* zeros, void* values, void* stream);
+
+/* Formats of the product's weights: INT4 as above, or MXFP4 as moe_layer takes it (E2M1 codes, a
+ * UE8M0 byte per 32 weights, row-major; byte 255 is NaN). */
+typedef enum { MOE_W4_INT4 = 0, MOE_W4_MXFP4 = 1 } moe_w4_format;
+
+typedef struct {
+  int32_t rows;           /* rows of A and C, 0 to 2^30 */
+  int32_t n;              /* N, columns of C, 1 to 2^23 */
+  int32_t k;              /* K, at most 2^20, a multiple of the group */
+  int32_t groups;         /* weight matrices (experts), 1 to 1024 */
+  int32_t weight_format;  /* moe_w4_format */
+  int32_t group_size;     /* G: 32, 64 or a multiple of 128; 32 for MXFP4 */
+  int32_t scale_dtype;    /* moe_dtype: bf16, f16 or f32; MOE_DT_U8 for MXFP4 */
+  int32_t zeros;          /* 1: INT4 with zero points */
+  int32_t dtype;          /* moe_dtype of A: bf16 or f16 */
+  int32_t out_dtype;      /* moe_dtype of C: bf16, f16 or f32 */
+  int32_t activation;     /* -1: none; or a moe_act */
+  float act_clamp;        /* MOE_ACT_SWIGLU_OAI: as in moe_layer_desc */
+  float act_alpha;
+  float act_up_bias;
+  int64_t a_stride;       /* elements between rows of A; 0 = K */
+  int64_t out_stride;     /* elements between rows of C; 0 = N */
+} moe_w4_gemm_desc;
+
+/* Grouped product of 16-bit rows with 4-bit weights for few rows per group (decoding), the weights
+ * read once for every 64 rows or fewer:
+ *   c[r, n] = sum_k a[r, k] * w[e, n, k]   for offsets[e] <= r < offsets[e + 1]
+ * or, with an activation, w holding 2N rows per group (gate [0, N), up [N, 2N)), the layer's
+ *   c[r, n] = act(sum_k a[r, k] * w[e, n, k], sum_k a[r, k] * w[e, N + n, k])
+ * a [rows, K] (say, tokens in expert order), b the codes [groups, N or 2N, K/2], b_scales and
+ * b_zeros [groups, N or 2N, K/G], offsets int32 [groups + 1] on the device, ascending from 0
+ * (moe_sort_tokens) and cut to [0, rows], or NULL with one group: all rows.  Rows of c in no group
+ * are left as they were.  Descending offsets give unspecified results, but no access outside the
+ * tensors.  Products are exact, sums float32 in an order that depends on the sizes only, the scale is
+ * applied to each group's sum in float32, and the result is rounded once to the type of C.
+ * b 16-byte aligned, the rest to their elements; b_zeros NULL without zero points; c must not
+ * overlap the inputs.  No workspace.  Stream, validation and error rules are those at the top of
+ * this file; rows = 0 launches nothing. */
+moe_status moe_w4_gemm(const moe_w4_gemm_desc* desc, const void* a, const uint8_t* b, const void* b_scales,
+                       const uint8_t* b_zeros, const int32_t* offsets, void* c, void* stream);
 
 #ifdef __cplusplus
 }

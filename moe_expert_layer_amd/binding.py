@@ -40,6 +40,10 @@ class MoeLayerDesc(ctypes.Structure):
 
 MOE_DT_BF16, MOE_DT_F16, MOE_DT_F32, MOE_DT_U8 = range(4)
 DTYPES = {"bf16": MOE_DT_BF16, "f16": MOE_DT_F16, "f32": MOE_DT_F32, "u8": MOE_DT_U8}
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+MOE_W4_INT4, MOE_W4_MXFP4 = 0, 1
+W4_FORMATS = {"int4": MOE_W4_INT4, "mxfp4": MOE_W4_MXFP4}
 
 
 class MoeDispatchDesc(ctypes.Structure):
@@ -60,6 +64,25 @@ class MoeMxfp4GemmDesc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("groups", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("a_scale_layout", ctypes.c_int32), ("b_scale_layout", ctypes.c_int32),
                 ("variant", ctypes.c_int32), ("out_stride", ctypes.c_int64)]
+
+
+class MoeBalanceDesc(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_experts", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("num_seqs", ctypes.c_int32), ("dtype", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("logit_stride", ctypes.c_int64), ("grad_stride", ctypes.c_int64)]
+
+
+class MoeInt4Desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("k", ctypes.c_int32), ("group", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int32), ("zeros", ctypes.c_int32), ("stride", ctypes.c_int64)]
+
+
+class MoeW4GemmDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("weight_format", ctypes.c_int32), ("group_size", ctypes.c_int32), ("scale_dtype", ctypes.c_int32),
+                ("zeros", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("act_clamp", ctypes.c_float), ("act_alpha", ctypes.c_float),
+                ("act_up_bias", ctypes.c_float), ("a_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
 
 
 class MoeError(RuntimeError):
@@ -117,6 +140,12 @@ def lib():
             "moe_quantize_mxfp4": [ctypes.POINTER(MoeMxfp4Desc), P, P, P, VP],
             "moe_dequantize_mxfp4": [ctypes.POINTER(MoeMxfp4Desc), P, P, P, VP],
             "moe_mxfp4_gemm": [ctypes.POINTER(MoeMxfp4GemmDesc), P, P, P, P, P, P, VP],
+            "moe_balance_workspace_size": [ctypes.POINTER(MoeBalanceDesc), ctypes.POINTER(ctypes.c_size_t)],
+            "moe_balance_loss": [ctypes.POINTER(MoeBalanceDesc), P, P, P, P, P, P, P, P, P, P, S, VP],
+            "moe_balance_loss_backward": [ctypes.POINTER(MoeBalanceDesc), P, P, P, P, P, P, P, P, P, VP],
+            "moe_quantize_int4": [ctypes.POINTER(MoeInt4Desc), P, P, P, P, VP],
+            "moe_dequantize_int4": [ctypes.POINTER(MoeInt4Desc), P, P, P, P, VP],
+            "moe_w4_gemm": [ctypes.POINTER(MoeW4GemmDesc), P, P, P, P, P, P, VP],
         }.items():
             f = getattr(L, name)
             f.restype, f.argtypes = I32, args
@@ -292,7 +321,7 @@ class _Torch:
         import torch
         self.raw_stream, self.current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         self.device = torch.cuda.device
-        self.i32, self.f32, self.u8 = torch.int32, torch.float32, torch.uint8
+        self.i32, self.f32, self.u8, self.bool = torch.int32, torch.float32, torch.uint8, torch.bool
         self.dtypes = {MOE_DT_BF16: torch.bfloat16, MOE_DT_F16: torch.float16, MOE_DT_F32: torch.float32,
                        MOE_DT_U8: torch.uint8}
 
@@ -523,3 +552,159 @@ def moe_mxfp4_gemm(desc, a, a_sf, b, b_sf, offsets, c, stream=None):
     _rows_tensor("c", c, v.dtype, v.rows, v.n, v.stride, dev)
     _launch(lib().moe_mxfp4_gemm, dev, stream, ctypes.byref(desc), a.data_ptr(), a_sf.data_ptr(), b.data_ptr(),
             b_sf.data_ptr(), _ptr(offsets), c.data_ptr())
+
+
+def make_balance_desc(num_tokens: int, num_experts: int, topk: int, num_seqs: int = 1, dtype: str = "f32",
+                      score: str = "softmax", logit_stride: int = 0, grad_stride: int = 0) -> MoeBalanceDesc:
+    """Descriptor of the router's balance loss.  dtype of the logits: "bf16", "f16" or "f32"; score: "softmax" or
+    "sigmoid" (of each logit, over the token's sum); strides in elements (0 = num_experts)."""
+    return MoeBalanceDesc(num_tokens, num_experts, topk, num_seqs, DTYPES[dtype], SCORES[score], logit_stride, grad_stride)
+
+
+def moe_balance_workspace_size(desc: MoeBalanceDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_balance_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_balance_workspace(desc: MoeBalanceDesc, device="cuda"):
+    """A uint8 device tensor of moe_balance_workspace_size(desc) bytes."""
+    import torch
+    return torch.empty(max(moe_balance_workspace_size(desc), 256), dtype=torch.uint8, device=device)
+
+
+class _BalanceView:
+    def __init__(self, d):
+        T = _torch()
+        self.i32, self.f32, self.u8, self.bool, self.dtype = T.i32, T.f32, T.u8, T.bool, _torch_dtype(d.dtype)
+        self.rows, self.cols, self.slots, self.seqs = d.num_tokens, d.num_experts, d.num_tokens * d.topk, d.num_seqs
+        self.logit_stride, self.grad_stride = d.logit_stride or d.num_experts, d.grad_stride or d.num_experts
+
+    def inputs(self, logits, mask, seq_offsets, dev):
+        _rows_tensor("logits", logits, self.dtype, self.rows, self.cols, self.logit_stride, dev)
+        if mask is not None:
+            _array("mask", mask, self.bool if mask.dtype is self.bool else self.u8, self.rows, dev)
+        if seq_offsets is not None:
+            _array("seq_offsets", seq_offsets, self.i32, self.seqs + 1, dev)
+
+
+def moe_balance_loss(desc, logits, topk_ids, counts, tokens, prob_sums, balance, workspace, z=None, mask=None,
+                     seq_offsets=None, stream=None):
+    """Counts int32 [S, E_tot], tokens int32 [S], prob_sums [S, E_tot], the balance loss [S] and, where given, the z loss
+    [S] of the routing logits [T, E_tot] and the experts chosen, topk_ids int32 [T, k].  mask (bool or uint8 [T]): the
+    tokens that count; seq_offsets int32 [S + 1]: the sequences' tokens (None: one sequence of all tokens)."""
+    v, dev = _view(_BalanceView, desc), _device_of(logits)
+    v.inputs(logits, mask, seq_offsets, dev)
+    _array("topk_ids", topk_ids, v.i32, v.slots, dev)
+    _array("counts", counts, v.i32, v.seqs * v.cols, dev)
+    _array("tokens", tokens, v.i32, v.seqs, dev)
+    _array("prob_sums", prob_sums, v.f32, v.seqs * v.cols, dev)
+    _array("balance", balance, v.f32, v.seqs, dev)
+    if z is not None:
+        _array("z", z, v.f32, v.seqs, dev)
+    _array("workspace", workspace, v.u8, 0, dev)
+    _launch(lib().moe_balance_loss, dev, stream, ctypes.byref(desc), logits.data_ptr(), topk_ids.data_ptr(), _ptr(mask),
+            _ptr(seq_offsets), counts.data_ptr(), tokens.data_ptr(), prob_sums.data_ptr(), balance.data_ptr(), _ptr(z),
+            workspace.data_ptr(), workspace.numel())
+
+
+def moe_balance_loss_backward(desc, logits, counts, tokens, dbalance, dlogits, dz=None, mask=None, seq_offsets=None,
+                              add=None, stream=None):
+    """Gradient of the routing logits: dlogits [T, E_tot] float32 = add (dlogits itself, say, or None) + the gradient of
+    sum_s dbalance[s] * balance[s] + dz[s] * z[s], from the counts and tokens of moe_balance_loss."""
+    v, dev = _view(_BalanceView, desc), _device_of(logits)
+    v.inputs(logits, mask, seq_offsets, dev)
+    _array("counts", counts, v.i32, v.seqs * v.cols, dev)
+    _array("tokens", tokens, v.i32, v.seqs, dev)
+    _array("dbalance", dbalance, v.f32, v.seqs, dev)
+    if dz is not None:
+        _array("dz", dz, v.f32, v.seqs, dev)
+    for name, t in (("add", add), ("dlogits", dlogits)):
+        if t is not None:
+            _rows_tensor(name, t, v.f32, v.rows, v.cols, v.grad_stride, dev)
+    _launch(lib().moe_balance_loss_backward, dev, stream, ctypes.byref(desc), logits.data_ptr(), _ptr(mask),
+            _ptr(seq_offsets), counts.data_ptr(), tokens.data_ptr(), dbalance.data_ptr(), _ptr(dz), _ptr(add),
+            dlogits.data_ptr())
+
+
+def make_int4_desc(rows: int, k: int, group: int = 128, dtype: str = "bf16", scale_dtype: str = "bf16",
+                   zeros: bool = False, stride: int = 0) -> MoeInt4Desc:
+    """Descriptor of 4-bit rows with a scale (and a zero point) per group, and the values they come from.  dtype,
+    scale_dtype: "bf16", "f16" or "f32"; group: 32, 64 or a multiple of 128; stride: elements between rows of the values
+    (0 = k)."""
+    return MoeInt4Desc(rows, k, group, DTYPES[dtype], DTYPES[scale_dtype], int(zeros), stride)
+
+
+def make_w4_gemm_desc(rows: int, n: int, k: int, groups: int = 1, weight_format: str = "int4", group_size: int = 128,
+                      scale_dtype: str = "bf16", zeros: bool = False, dtype: str = "bf16", out_dtype: str = "bf16",
+                      activation: Optional[str] = None, activation_clamp: Optional[float] = None,
+                      activation_alpha: float = 1.0, activation_up_bias: float = 0.0, a_stride: int = 0,
+                      out_stride: int = 0) -> MoeW4GemmDesc:
+    """Descriptor of a grouped product of 16-bit rows [rows, k] with 4-bit weights [groups, n, k] -> [rows, n]; with an
+    activation ("swiglu", "swigluoai") the weights are [groups, 2n, k], gate rows before up rows.  weight_format: "int4",
+    or "mxfp4" (group_size 32, scale_dtype "ue8m0")."""
+    return MoeW4GemmDesc(rows, n, k, groups, W4_FORMATS[weight_format], group_size,
+                         MOE_DT_U8 if scale_dtype == "ue8m0" else DTYPES[scale_dtype], int(zeros), DTYPES[dtype],
+                         DTYPES[out_dtype], -1 if activation is None else ACTIVATIONS[activation],
+                         math.inf if activation_clamp is None else activation_clamp, activation_alpha,
+                         activation_up_bias, a_stride, out_stride)
+
+
+class _Int4View:
+    def __init__(self, d):
+        self.rows, self.k, self.stride, self.codes = d.rows, d.k, d.stride or d.k, d.rows * (d.k // 2)
+        self.n = d.rows * (d.k // d.group) if d.group > 0 else 0
+        self.dtype, self.scale, self.u8, self.zeros = _torch_dtype(d.dtype), _torch_dtype(d.scale_dtype), _torch().u8, d.zeros
+
+    def check(self, values, codes, scales, zeros, dev):
+        _rows_tensor("values", values, self.dtype, self.rows, self.k, self.stride, dev)
+        _array("codes", codes, self.u8, self.codes, dev)
+        _array("scales", scales, self.scale, self.n, dev)
+        if zeros is not None:
+            _array("zeros", zeros, self.u8, self.n, dev)
+
+
+class _W4GemmView:
+    def __init__(self, d):
+        self.rows, self.n, self.k, self.offsets = d.rows, d.n, d.k, d.groups + 1
+        self.a_stride, self.out_stride = d.a_stride or d.k, d.out_stride or d.n
+        b_rows = d.groups * d.n * (1 if d.activation < 0 else 2)
+        self.codes, self.scales_n = b_rows * (d.k // 2), b_rows * (d.k // d.group_size) if d.group_size > 0 else 0
+        self.dtype, self.out, self.scale = _torch_dtype(d.dtype), _torch_dtype(d.out_dtype), _torch_dtype(d.scale_dtype)
+        self.u8, self.i32 = _torch().u8, _torch().i32
+
+
+def moe_quantize_int4(desc, values, codes, scales, zeros=None, stream=None):
+    """values [rows, k] -> codes uint8 [rows, k / 2], scales [rows, k / group] and, where the descriptor has them, zero
+    points uint8 [rows, k / group]."""
+    v, dev = _view(_Int4View, desc), _device_of(values)
+    v.check(values, codes, scales, zeros, dev)
+    _launch(lib().moe_quantize_int4, dev, stream, ctypes.byref(desc), values.data_ptr(), codes.data_ptr(),
+            scales.data_ptr(), _ptr(zeros))
+
+
+def moe_dequantize_int4(desc, codes, scales, zeros, values, dtype: Optional[str] = None, stream=None):
+    """The values [rows, k] of codes, scales and zero points (or None), in the descriptor's dtype (or the one named)."""
+    if dtype is not None and DTYPES[dtype] != desc.dtype:
+        desc = MoeInt4Desc(desc.rows, desc.k, desc.group, DTYPES[dtype], desc.scale_dtype, desc.zeros, desc.stride)
+    v, dev = _view(_Int4View, desc), _device_of(codes)
+    v.check(values, codes, scales, zeros, dev)
+    _launch(lib().moe_dequantize_int4, dev, stream, ctypes.byref(desc), codes.data_ptr(), scales.data_ptr(), _ptr(zeros),
+            values.data_ptr())
+
+
+def moe_w4_gemm(desc, a, b, b_scales, b_zeros, offsets, c, stream=None):
+    """c[r] = a[r] @ w[e].T (with an activation: act of the gate and up halves) for the rows of each group e (offsets
+    int32 [groups + 1]; None: one group of all rows), w the values of b, b_scales and b_zeros (None without zero
+    points).  Rows past the last group are left as they were."""
+    v, dev = _view(_W4GemmView, desc), _device_of(a)
+    _rows_tensor("a", a, v.dtype, v.rows, v.k, v.a_stride, dev)
+    _array("b", b, v.u8, v.codes, dev)
+    _array("b_scales", b_scales, v.scale, v.scales_n, dev)
+    if b_zeros is not None:
+        _array("b_zeros", b_zeros, v.u8, v.scales_n, dev)
+    if offsets is not None:
+        _array("offsets", offsets, v.i32, v.offsets, dev)
+    _rows_tensor("c", c, v.out, v.rows, v.n, v.out_stride, dev)
+    _launch(lib().moe_w4_gemm, dev, stream, ctypes.byref(desc), a.data_ptr(), b.data_ptr(), b_scales.data_ptr(),
+            _ptr(b_zeros), _ptr(offsets), c.data_ptr())

@@ -738,4 +738,219 @@ moe_status moe_mxfp4_gemm(const moe_mxfp4_gemm_desc* d, const uint8_t* a, const 
   return ok();
 }
 
+// ---------------------------------------------------------------------------------------
+// the router's balance loss
+
+namespace {
+
+constexpr int kMaxSeqs = 1 << 16;
+
+moe_status check_balance_desc(const moe_balance_desc* d) {
+  if (!d) return fail(MOE_ERR_NULL, "desc is NULL");
+  if (d->num_tokens < 0) return fail(MOE_ERR_INVALID_DESC, "num_tokens %d < 0", d->num_tokens);
+  if (d->num_experts < 1 || d->num_experts > moe::kMaxExperts)
+    return fail(MOE_ERR_INVALID_DESC, "num_experts %d outside [1, %d]", d->num_experts, moe::kMaxExperts);
+  if (d->topk < 1 || d->topk > moe::kMaxTopk)
+    return fail(MOE_ERR_INVALID_DESC, "topk %d outside [1, %d]", d->topk, moe::kMaxTopk);
+  if ((long long)d->num_tokens * d->topk > kMaxSlots)
+    return fail(MOE_ERR_INVALID_DESC, "num_tokens * topk must be at most 2^31 - 2^17");
+  if (d->num_seqs < 1 || d->num_seqs > kMaxSeqs)
+    return fail(MOE_ERR_INVALID_DESC, "num_seqs %d outside [1, %d]", d->num_seqs, kMaxSeqs);
+  if (d->dtype != MOE_DT_BF16 && d->dtype != MOE_DT_F16 && d->dtype != MOE_DT_F32)
+    return fail(MOE_ERR_INVALID_DESC, "dtype %d is not bf16, f16 or f32", d->dtype);
+  if (d->score != MOE_SCORE_SOFTMAX && d->score != MOE_SCORE_SIGMOID)
+    return fail(MOE_ERR_INVALID_DESC, "score %d unknown", d->score);
+  for (const long long stride : {(long long)d->logit_stride, (long long)d->grad_stride})
+    if (stride != 0 && (stride < d->num_experts || stride > kMaxStride))
+      return fail(MOE_ERR_INVALID_DESC, "stride %lld neither 0 nor in [num_experts, 2^40]", stride);
+  return MOE_OK;
+}
+
+// what both calls ask of the tensors that both take
+moe_status check_balance_inputs(const moe_balance_desc* d, const void* logits, const int32_t* offsets, const float* z) {
+  if (z && d->score == MOE_SCORE_SIGMOID) return fail(MOE_ERR_UNSUPPORTED, "the z loss goes with softmax scores");
+  if (!offsets && d->num_seqs != 1) return fail(MOE_ERR_NULL, "seq_offsets NULL with %d sequences", d->num_seqs);
+  if (misaligned(logits, (size_t)moe::dtype_bytes(d->dtype)) || misaligned(offsets, 4) || misaligned(z, 4))
+    return fail(MOE_ERR_MISALIGNED, "logits / seq_offsets / z not aligned to their elements");
+  return MOE_OK;
+}
+
+moe::BalanceShape balance_shape(const moe_balance_desc& d) {
+  moe::BalanceShape b;
+  b.T = d.num_tokens; b.E = d.num_experts; b.k = d.topk; b.S = d.num_seqs; b.dtype = d.dtype;
+  b.sigmoid = d.score == MOE_SCORE_SIGMOID;
+  b.logit_stride = d.logit_stride ? d.logit_stride : d.num_experts;
+  b.grad_stride = d.grad_stride ? d.grad_stride : d.num_experts;
+  return b;
+}
+
+}  // namespace
+
+moe_status moe_balance_workspace_size(const moe_balance_desc* d, size_t* bytes) {
+  if (moe_status st = check_balance_desc(d)) return st;
+  if (!bytes) return fail(MOE_ERR_NULL, "bytes is NULL");
+  *bytes = align_up(moe::balance_workspace(d->num_tokens, d->num_experts, d->num_seqs));
+  return ok();
+}
+
+moe_status moe_balance_loss(const moe_balance_desc* d, const void* logits, const int32_t* ids, const uint8_t* opt_mask,
+                            const int32_t* opt_offsets, int32_t* counts, int32_t* tokens, float* psum, float* balance,
+                            float* opt_z, void* ws, size_t ws_bytes, void* stream) {
+  if (moe_status st = check_balance_desc(d)) return st;
+  if (d->num_tokens == 0) return ok();
+  if (!logits || !ids || !counts || !tokens || !psum || !balance)
+    return fail(MOE_ERR_NULL, "logits/topk_ids/counts/tokens/prob_sums/balance NULL");
+  if (moe_status st = check_balance_inputs(d, logits, opt_offsets, opt_z)) return st;
+  if (misaligned(ids, 4) || misaligned(counts, 4) || misaligned(tokens, 4) || misaligned(psum, 4) || misaligned(balance, 4))
+    return fail(MOE_ERR_MISALIGNED, "topk_ids / counts / tokens / prob_sums / balance not 4-byte aligned");
+  const size_t need = align_up(moe::balance_workspace(d->num_tokens, d->num_experts, d->num_seqs));
+  if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+  if (misaligned(ws, kAlign)) return fail(MOE_ERR_MISALIGNED, "workspace not 256-byte aligned");
+  if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes < required %zu", ws_bytes, need);
+  if (moe_status st = check_device()) return st;
+  MOE_TRY_HIP(moe::launch_balance(balance_shape(*d), logits, ids, opt_mask, opt_offsets, counts, tokens, psum, balance,
+                                  opt_z, ws, (hipStream_t)stream));
+  return ok();
+}
+
+moe_status moe_balance_loss_backward(const moe_balance_desc* d, const void* logits, const uint8_t* opt_mask,
+                                     const int32_t* opt_offsets, const int32_t* counts, const int32_t* tokens,
+                                     const float* dbalance, const float* opt_dz, const float* opt_add, float* dlogits,
+                                     void* stream) {
+  if (moe_status st = check_balance_desc(d)) return st;
+  if (d->num_tokens == 0) return ok();
+  if (!logits || !counts || !tokens || !dbalance || !dlogits)
+    return fail(MOE_ERR_NULL, "logits/counts/tokens/dbalance/dlogits NULL");
+  if (moe_status st = check_balance_inputs(d, logits, opt_offsets, opt_dz)) return st;
+  if (misaligned(counts, 4) || misaligned(tokens, 4) || misaligned(dbalance, 4) || misaligned(opt_add, 4) ||
+      misaligned(dlogits, 4))
+    return fail(MOE_ERR_MISALIGNED, "counts / tokens / dbalance / add / dlogits not 4-byte aligned");
+  if (moe_status st = check_device()) return st;
+  MOE_TRY_HIP(moe::launch_balance_backward(balance_shape(*d), logits, opt_mask, opt_offsets, counts, tokens, dbalance,
+                                           opt_dz, opt_add, dlogits, (hipStream_t)stream));
+  return ok();
+}
+
+// ---------------------------------------------------------------------------------------
+// 4-bit weights with group scales
+
+namespace {
+
+constexpr int kMaxW4N = 1 << 23;
+
+moe_status check_w4_k(int32_t k, int32_t group) {
+  if (group != 32 && group != 64 && (group < 128 || group % 128))
+    return fail(MOE_ERR_INVALID_DESC, "group %d is not 32, 64 or a multiple of 128", group);
+  if (k < 1 || k % group || k > kMaxMxK)
+    return fail(MOE_ERR_INVALID_DESC, "k %d not a positive multiple of the group %d up to %d", k, group, kMaxMxK);
+  return MOE_OK;
+}
+
+moe_status check_zeros(int32_t zeros, const void* p) {
+  if (zeros && !p) return fail(MOE_ERR_NULL, "zeros NULL, the descriptor has zero points");
+  if (!zeros && p) return fail(MOE_ERR_INVALID_DESC, "zeros given, the descriptor has no zero points");
+  return MOE_OK;
+}
+
+moe_status check_int4_call(const moe_int4_desc* d, const void* values, const void* codes, const void* scales,
+                           const void* zeros) {
+  if (!d) return fail(MOE_ERR_NULL, "desc is NULL");
+  if (d->rows < 0 || d->rows > kMaxMxRows)
+    return fail(MOE_ERR_INVALID_DESC, "rows %d outside [0, %d]", d->rows, kMaxMxRows);
+  if (moe_status st = check_w4_k(d->k, d->group)) return st;
+  if (moe_status st = check_mx_float(d->dtype)) return st;
+  if (moe_status st = check_mx_float(d->scale_dtype)) return st;
+  if (d->zeros != 0 && d->zeros != 1) return fail(MOE_ERR_INVALID_DESC, "zeros %d is not 0 or 1", d->zeros);
+  if (d->stride != 0 && (d->stride < d->k || d->stride > kMaxStride))
+    return fail(MOE_ERR_INVALID_DESC, "stride %lld neither 0 nor in [k, 2^40]", (long long)d->stride);
+  if (d->rows == 0) return MOE_OK;
+  if (!values || !codes || !scales) return fail(MOE_ERR_NULL, "values/codes/scales NULL");
+  if (moe_status st = check_zeros(d->zeros, zeros)) return st;
+  if (misaligned(values, (size_t)moe::dtype_bytes(d->dtype)) || misaligned(codes, 16) ||
+      misaligned(scales, (size_t)moe::dtype_bytes(d->scale_dtype)))
+    return fail(MOE_ERR_MISALIGNED, "values / codes / scales misaligned");
+  return MOE_OK;
+}
+
+moe::Int4Shape int4_shape(const moe_int4_desc& d) {
+  moe::Int4Shape s;
+  s.M = d.rows; s.K = d.k; s.G = d.group; s.dtype = d.dtype; s.scale_dtype = d.scale_dtype; s.zeros = d.zeros != 0;
+  s.stride = d.stride ? d.stride : d.k;
+  return s;
+}
+
+}  // namespace
+
+moe_status moe_quantize_int4(const moe_int4_desc* d, const void* values, uint8_t* codes, void* scales, uint8_t* zeros,
+                             void* stream) {
+  if (moe_status st = check_int4_call(d, values, codes, scales, zeros)) return st;
+  if (d->rows == 0) return ok();
+  if (moe_status st = check_device()) return st;
+  MOE_TRY_HIP(moe::launch_quantize_int4(int4_shape(*d), values, codes, scales, zeros, (hipStream_t)stream));
+  return ok();
+}
+
+moe_status moe_dequantize_int4(const moe_int4_desc* d, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                               void* values, void* stream) {
+  if (moe_status st = check_int4_call(d, values, codes, scales, zeros)) return st;
+  if (d->rows == 0) return ok();
+  if (moe_status st = check_device()) return st;
+  MOE_TRY_HIP(moe::launch_dequantize_int4(int4_shape(*d), codes, scales, zeros, values, (hipStream_t)stream));
+  return ok();
+}
+
+moe_status moe_w4_gemm(const moe_w4_gemm_desc* d, const void* a, const uint8_t* b, const void* b_scales,
+                       const uint8_t* b_zeros, const int32_t* offsets, void* c, void* stream) {
+  if (!d) return fail(MOE_ERR_NULL, "desc is NULL");
+  if (d->rows < 0 || d->rows > kMaxMxRows)
+    return fail(MOE_ERR_INVALID_DESC, "rows %d outside [0, %d]", d->rows, kMaxMxRows);
+  if (d->n < 1 || d->n > kMaxW4N) return fail(MOE_ERR_INVALID_DESC, "n %d outside [1, %d]", d->n, kMaxW4N);
+  if (d->groups < 1 || d->groups > kMaxMxGroups)
+    return fail(MOE_ERR_INVALID_DESC, "groups %d outside [1, %d]", d->groups, kMaxMxGroups);
+  if ((long long)d->groups * d->n > kMaxMxRows / 2)
+    return fail(MOE_ERR_INVALID_DESC, "groups * n above %d", kMaxMxRows / 2);
+  if (moe_status st = check_w4_k(d->k, d->group_size)) return st;
+  const bool mx = d->weight_format == MOE_W4_MXFP4;
+  if (!mx && d->weight_format != MOE_W4_INT4)
+    return fail(MOE_ERR_INVALID_DESC, "weight_format %d unknown", d->weight_format);
+  if (mx) {
+    if (d->group_size != 32 || d->scale_dtype != MOE_DT_U8 || d->zeros)
+      return fail(MOE_ERR_INVALID_DESC, "MXFP4 weights have groups of 32, UE8M0 scale bytes and no zero points");
+  } else if (moe_status st = check_mx_float(d->scale_dtype)) {
+    return st;
+  }
+  if (d->zeros != 0 && d->zeros != 1) return fail(MOE_ERR_INVALID_DESC, "zeros %d is not 0 or 1", d->zeros);
+  if (d->dtype != MOE_DT_BF16 && d->dtype != MOE_DT_F16)
+    return fail(MOE_ERR_INVALID_DESC, "dtype %d is not bf16 or f16", d->dtype);
+  if (moe_status st = check_mx_float(d->out_dtype)) return st;
+  if (d->activation < -1 || d->activation > MOE_ACT_SWIGLU_OAI)
+    return fail(MOE_ERR_INVALID_DESC, "activation %d unknown", d->activation);
+  if (d->activation == MOE_ACT_SWIGLU_OAI) {
+    if (!(d->act_clamp > 0.f)) return fail(MOE_ERR_INVALID_DESC, "act_clamp must be > 0 (or +inf)");
+    if (!std::isfinite(d->act_alpha) || !std::isfinite(d->act_up_bias))
+      return fail(MOE_ERR_INVALID_DESC, "act_alpha / act_up_bias must be finite");
+  }
+  if (d->a_stride != 0 && (d->a_stride < d->k || d->a_stride > kMaxStride))
+    return fail(MOE_ERR_INVALID_DESC, "a_stride %lld neither 0 nor in [k, 2^40]", (long long)d->a_stride);
+  if (d->out_stride != 0 && (d->out_stride < d->n || d->out_stride > kMaxStride))
+    return fail(MOE_ERR_INVALID_DESC, "out_stride %lld neither 0 nor in [n, 2^40]", (long long)d->out_stride);
+  if (d->rows == 0) return ok();
+  if (!a || !b || !b_scales || !c) return fail(MOE_ERR_NULL, "a/b/b_scales/c NULL");
+  if (moe_status st = check_zeros(d->zeros, b_zeros)) return st;
+  if (!offsets && d->groups != 1) return fail(MOE_ERR_NULL, "offsets NULL with %d groups", d->groups);
+  if (misaligned(a, 2) || misaligned(b, 16) || misaligned(b_scales, (size_t)moe::dtype_bytes(d->scale_dtype)) ||
+      misaligned(offsets, 4) || misaligned(c, (size_t)moe::dtype_bytes(d->out_dtype)))
+    return fail(MOE_ERR_MISALIGNED, "a / b / b_scales / offsets / c misaligned");
+  if (moe_status st = check_device()) return st;
+  moe::W4GemmArgs g{};
+  g.A = a; g.B = b; g.scales = b_scales; g.zeros = b_zeros; g.offsets = offsets; g.C = c;
+  g.a_stride = d->a_stride ? d->a_stride : d->k;
+  g.c_stride = d->out_stride ? d->out_stride : d->n;
+  g.rows = d->rows; g.N = d->n; g.K = d->k; g.groups = d->groups; g.G = d->group_size;
+  g.scale_dtype = d->scale_dtype; g.out_dtype = d->out_dtype;
+  g.act = d->activation; g.clamp = d->act_clamp; g.alpha = d->act_alpha; g.bias = d->act_up_bias;
+  MOE_TRY_HIP(moe::launch_w4_gemm(g, d->dtype, mx, (hipStream_t)stream));
+  return ok();
+}
+
 }  // extern "C"
