@@ -20,6 +20,12 @@
 #include "elem.hpp"
 #include "operators.hpp"
 
+#ifndef STREAM_OCC
+#define STREAM_OCC 2
+#endif
+#ifndef STREAM_NT
+#define STREAM_NT 2
+#endif
 namespace moe {
 
 namespace {
@@ -53,16 +59,26 @@ __device__ __forceinline__ uint32_t from_e2m1(uint32_t v) {
   else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, 1.f, B));
 }
 
-// eight codes as 16-bit floats, in their order
-template <typename XT, int FMT>
+// eight codes as 16-bit floats, in their order; INT4 with TURNED: even ones, then odd ones, which saves two permutations where the
+// rows' values have been put in that order once for many weights (turn)
+template <typename XT, int FMT, bool TURNED>
 __device__ __forceinline__ u32x4 widen(uint32_t q) {
   if constexpr (FMT == kMxfp4) {
     return u32x4{from_e2m1<XT, 0>(q), from_e2m1<XT, 1>(q), from_e2m1<XT, 2>(q), from_e2m1<XT, 3>(q)};
   } else {
     const uint32_t even = q & 0x0f0f0f0fu, odd = (q >> 4) & 0x0f0f0f0fu;
+    if constexpr (TURNED)
+      return u32x4{from_e4m3<XT, false>(even), from_e4m3<XT, true>(even), from_e4m3<XT, false>(odd), from_e4m3<XT, true>(odd)};
     const uint32_t a = __builtin_amdgcn_perm(odd, even, 0x05010400u), b = __builtin_amdgcn_perm(odd, even, 0x07030602u);
     return u32x4{from_e4m3<XT, false>(a), from_e4m3<XT, true>(a), from_e4m3<XT, false>(b), from_e4m3<XT, true>(b)};
   }
+}
+template <int FMT>
+__device__ __forceinline__ u32x4 turn(u32x4 x) {
+  if constexpr (FMT == kMxfp4) return x;
+  constexpr uint32_t lo = 0x05040100u, hi = 0x07060302u;
+  return u32x4{__builtin_amdgcn_perm(x[1], x[0], lo), __builtin_amdgcn_perm(x[3], x[2], lo),
+               __builtin_amdgcn_perm(x[1], x[0], hi), __builtin_amdgcn_perm(x[3], x[2], hi)};
 }
 
 // out_j of quarter i = d_i of quarter j
@@ -74,10 +90,14 @@ __device__ __forceinline__ u32x4 transpose_quarters(u32x4 d) {
   return u32x4{lo[0], lo[1], hi[0], hi[1]};
 }
 
-// a stored scale's bits as a float: a UE8M0 byte, float16 or bfloat16, float32
+// a stored scale's bits as a float: a UE8M0 byte (255, NaN, becomes an infinity, which makes the results not finite, and those
+// are taken again), float16 or bfloat16, float32
 template <int SIZE>
 __device__ __forceinline__ float scale_value(uint32_t raw, int dtype) {
-  if constexpr (SIZE == 1) return __uint_as_float(raw == 0 ? 0x00400000u : raw == 255 ? 0x7fc00000u : raw << 23);
+  if constexpr (SIZE == 1) {
+    const uint32_t v = raw << 23;
+    return __uint_as_float(v > 0x00400000u ? v : 0x00400000u);
+  }
   if constexpr (SIZE == 4) return __uint_as_float(raw);
   float h = Elem<F16>::get(F16{(uint16_t)raw}), b = __uint_as_float(raw << 16);
   asm("" : "+v"(h), "+v"(b));  // both and a choice, not a branch
@@ -114,7 +134,7 @@ __device__ __forceinline__ u32x4 load_row16(gptr p) {  // 16 bytes of a row of 1
   return *(const MOE_GLOBAL at2*)p;
 }
 
-// N (1, 2 or 4) consecutive items of SIZE bytes at any alignment of theirs, as they lie; `have`: the first ones only
+// N (a power of two) consecutive items of SIZE bytes at any alignment of theirs, as they lie; `have`: the first ones only
 template <int N, int SIZE>
 struct Items {
   static constexpr int kWords = (N * SIZE + 3) / 4;
@@ -130,11 +150,15 @@ struct Items {
       typedef uint32_t at1 __attribute__((aligned(1)));
       w[0] = *(const MOE_GLOBAL at1*)p;
     } else {
-      typedef uint32_t vec __attribute__((ext_vector_type(kWords)));
-      typedef vec at2 __attribute__((aligned(2)));
-      const vec v = *(const MOE_GLOBAL at2*)p;
+      constexpr int kStep = kWords < 4 ? kWords : 4;
+      typedef uint32_t vec __attribute__((ext_vector_type(kStep)));
+      typedef vec at1 __attribute__((aligned(1)));
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) w[i] = v[i];
+      for (int j = 0; j < kWords; j += kStep) {
+        const vec v = *(const MOE_GLOBAL at1*)(p + 4 * j);
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) w[j + i] = v[i];
+      }
     }
   }
   __device__ __forceinline__ void load(gptr p, int have) {
@@ -145,13 +169,33 @@ struct Items {
       if (i < have) {
         if constexpr (SIZE == 4) w[i] = ((const MOE_GLOBAL uint32_t*)p)[i];
         else if constexpr (SIZE == 2) w[i >> 1] |= (uint32_t)((const MOE_GLOBAL uint16_t*)p)[i] << (16 * (i & 1));
-        else w[0] |= (uint32_t)p[i] << (8 * i);
+        else w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
       }
+  }
+  __device__ __forceinline__ void load_lds(const uint8_t* p) {
+    if constexpr (N * SIZE == 1) w[0] = *p;
+    else if constexpr (N * SIZE == 2) w[0] = *reinterpret_cast<const uint16_t*>(p);
+    else
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  }
+  // whole ones of 4 items as far as there are `have`, and the rest one by one
+  __device__ __forceinline__ void load_first(gptr p, int have) {
+    if constexpr (N > 4) {
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        Items<4, SIZE> q = {};
+        if (have >= 4 * i + 4) q.load(p + 4 * SIZE * i);
+        else if (have > 4 * i) q.load(p + 4 * SIZE * i, have - 4 * i);
+#pragma unroll
+        for (int j = 0; j < SIZE; ++j) w[i * SIZE + j] = q.w[j];
+      }
+    }
   }
   __device__ __forceinline__ uint32_t get(int i) const {
     if constexpr (SIZE == 4) return w[i];
     else if constexpr (SIZE == 2) return (w[i >> 1] >> (16 * (i & 1))) & 0xffffu;
-    else return (w[0] >> (8 * i)) & 0xffu;
+    else return (w[i >> 2] >> (8 * (i & 3))) & 0xffu;
   }
 };
 
@@ -163,17 +207,30 @@ __device__ __forceinline__ int2 expert_rows(const int32_t* __restrict__ offsets,
 
 // One sum by the definition.  q times an infinity is infinite or NaN whatever z is, and so is z times the sum of x,
 // so where the sums taken apart are not finite, they are taken like this.
-template <typename XT>
+template <typename XT, int FMT>
 __device__ __forceinline__ float plain_sum(const XT* x, const uint8_t* q, const void* scales, const uint8_t* zeros,
-                                        long long at, int K, int G, int scale_dtype) {
+                                           long long at, int K, int G, int scale_dtype) {
   float acc = 0.f;
   for (int k0 = 0; k0 < K; k0 += G, ++at) {
     const float z = zeros != nullptr ? (float)zeros[at] : 8.f;
-    float sum = 0.f;
-    for (int k = k0; k < k0 + G; ++k)
-      sum = fmaf(Elem<XT>::get(x[k]), (float)((q[k >> 1] >> (4 * (k & 1))) & 15) - z, sum);
-    const float s = scale_dtype == 2 ? scale_value<4>(static_cast<const uint32_t*>(scales)[at], 2)
-                                     : scale_value<2>(static_cast<const uint16_t*>(scales)[at], scale_dtype);
+    float sum = 0.f, s;
+    for (int k = k0; k < k0 + G; ++k) {
+      const int c = (q[k >> 1] >> (4 * (k & 1))) & 15;
+      float w = (float)c - z;
+      if (FMT == kMxfp4) {
+        const int m = c & 7;
+        w = m < 4 ? m * 0.5f : m < 6 ? m - 2.f : 2.f * m - 8.f;  // 0 .5 1 1.5 2 3 4 6
+        w = c > 7 ? -w : w;
+      }
+      sum = fmaf(Elem<XT>::get(x[k]), w, sum);
+    }
+    if (FMT == kMxfp4) {
+      const uint32_t b = static_cast<const uint8_t*>(scales)[at];
+      s = b == 255 ? __uint_as_float(0x7fc00000u) : scale_value<1>(b, 0);
+    } else {
+      s = scale_dtype == 2 ? scale_value<4>(static_cast<const uint32_t*>(scales)[at], 2)
+                           : scale_value<2>(static_cast<const uint16_t*>(scales)[at], scale_dtype);
+    }
     acc = fmaf(s, sum, acc);
   }
   return acc;
@@ -191,7 +248,7 @@ __device__ __forceinline__ float activate(const W4GemmArgs& g, float gate, float
   return gate / (1.f + expf(-alpha * gate)) * up;
 }
 
-// Where a wave's weight rows lie: NT tiles of 16, or a gate and an up tile.  Uniform addresses, and 32-bit offsets of the lane's
+// Where a wave's weight rows lie: NT tiles of 16, or NT / 2 gate tiles and as many up tiles.  Uniform addresses, and 32-bit offsets of the lane's
 // row (cut to the expert's last one)
 template <int SIZE, int NT>
 struct Columns {
@@ -207,8 +264,9 @@ struct Columns {
     z_mul = g.zeros != nullptr ? 1 : 0;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int n = g.act >= 0 ? n0 : min(n0 + i * 16, g.N - 1);
-      first[i] = e * rows + n + (g.act >= 0 && i ? g.N : 0);
+      const bool up = g.act >= 0 && i >= NT / 2;
+      const int n = min(n0 + (up ? i - NT / 2 : i) * 16, g.N - 1);
+      first[i] = e * rows + n + (up ? g.N : 0);
       const uint32_t lane = min(r16, g.N - 1 - n);
       q[i] = uniform(g.B + first[i] * (g.K / 2));
       s[i] = uniform(static_cast<const uint8_t*>(g.scales) + first[i] * ng * SIZE);
@@ -219,6 +277,99 @@ struct Columns {
     }
   }
 };
+
+// Sums of a wave's tiles.  One group's sums wait until the matrix instructions of the next have been issued before they are
+// scaled and added, so that those few instructions do not wait for the matrix cores (with RT > 1 rows' tiles there are
+// enough of them in flight)
+template <int FMT, int RT, int NT>
+struct Sums {
+  static constexpr bool kWait = RT == 1;
+  v4f acc[RT][NT], p[RT][NT], x[RT];  // x: of the rows' values
+  float scale[NT], zero[NT];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int m = 0; m < RT; ++m) {
+      x[m] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < NT; ++s) acc[m][s] = p[m][s] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int s = 0; s < NT; ++s) scale[s] = zero[s] = 0.f;
+  }
+  __device__ __forceinline__ void add(const v4f (&q)[RT][NT], const v4f (&sx)[RT], const float (&sc)[NT], const float (&z)[NT]) {
+#pragma unroll
+    for (int s = 0; s < NT; ++s)
+#pragma unroll
+      for (int m = 0; m < RT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v = FMT == kInt4 ? fmaf(-z[s], sx[m][i], q[m][s][i]) : q[m][s][i];
+          acc[m][s][i] = fmaf(sc[s], v, acc[m][s][i]);
+        }
+  }
+  __device__ __forceinline__ void finish() {
+    if (kWait) add(p, x, scale, zero);
+  }
+};
+
+// The products of 128 of K.  q: codes; x(m, j): rows 16 m + lane % 16, the eight values of step j of this lane's quarter (asked for
+// a step ahead; v has those of step 0, and on return those of step 4); scale_of(s, f), zero_of(s, f): of tile s and fold f
+template <typename XT, int FMT, bool TURNED, int FOLD, int RT, int NT, typename X, typename S, typename Z>
+__device__ __forceinline__ void multiply(u32x4 (&q)[NT], u32x4 (&v)[RT], X x, S scale_of, Z zero_of, Sums<FMT, RT, NT>& sums) {
+  if constexpr (FOLD < 4) {
+#pragma unroll
+    for (int s = 0; s < NT; ++s) q[s] = transpose_quarters(q[s]);
+  }
+#pragma unroll
+  for (int f = 0; f < 4 / FOLD; ++f) {
+    v4f p[RT][NT], sx[RT];
+    float scale[NT], zero[NT];
+#pragma unroll
+    for (int m = 0; m < RT; ++m) {
+      sx[m] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < NT; ++s) p[m][s] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int i = 0; i < FOLD; ++i) {
+      const int j = f * FOLD + i;
+      __builtin_amdgcn_sched_barrier(0);  // one step's values in registers at a time
+      u32x4 w[NT], ahead[RT];
+#pragma unroll
+      for (int m = 0; m < RT; ++m) ahead[m] = x(m, j + 1);
+#pragma unroll
+      for (int s = 0; s < NT; ++s) w[s] = widen<XT, FMT, TURNED>(q[s][j]);
+#pragma unroll
+      for (int m = 0; m < RT; ++m) {
+#pragma unroll
+        for (int s = 0; s < NT; ++s) p[m][s] = mfma(XT{}, v[m], w[s], p[m][s]);
+        if constexpr (FMT == kInt4) sx[m] = mfma(XT{}, v[m], ones<XT>(), sx[m]);
+        v[m] = ahead[m];
+      }
+      if (Sums<FMT, RT, NT>::kWait && i == 0) {
+        __builtin_amdgcn_sched_barrier(0);
+        sums.add(sums.p, sums.x, sums.scale, sums.zero);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < NT; ++s) {
+      scale[s] = scale_of(s, f);
+      zero[s] = FMT == kInt4 ? zero_of(s, f) : 0.f;
+    }
+    if (!Sums<FMT, RT, NT>::kWait) {
+      sums.add(p, sx, scale, zero);
+    } else {
+#pragma unroll
+      for (int s = 0; s < NT; ++s) {
+        sums.p[0][s] = p[0][s];
+        sums.scale[s] = scale[s];
+        sums.zero[s] = zero[s];
+      }
+      sums.x[0] = sx[0];
+    }
+  }
+}
 
 // What a wave needs of the weights for 128 of K.  FOLD: 32-wide steps that go under one scale; SIZE: a scale's bytes
 template <int FMT, int SIZE, int FOLD, int NT>
@@ -247,53 +398,13 @@ struct Codes {
       }
     }
   }
+  template <typename XT, int RT, typename X>
+  __device__ __forceinline__ void multiply_into(const W4GemmArgs& g, u32x4 (&v)[RT], X x, Sums<FMT, RT, NT>& sums) {
+    multiply<XT, FMT, false, FOLD, RT, NT>(
+        q, v, x, [&](int t, int f) { return scale_value<SIZE>(s[t].get(f), g.scale_dtype); },
+        [&](int t, int f) { return g.zeros != nullptr ? (float)z[t].get(f) : 8.f; }, sums);
+  }
 };
-
-// acc += the products of 128 of K.  x(m, j): rows 16 m + lane % 16, the eight values of step j of this lane's quarter
-template <typename XT, int FMT, int SIZE, int FOLD, int RT, int NT, typename X>
-__device__ __forceinline__ void multiply(const W4GemmArgs& g, Codes<FMT, SIZE, FOLD, NT>& t, X x, v4f (&acc)[RT][NT]) {
-  if constexpr (FOLD < 4) {
-#pragma unroll
-    for (int s = 0; s < NT; ++s) t.q[s] = transpose_quarters(t.q[s]);
-  }
-#pragma unroll
-  for (int f = 0; f < 4 / FOLD; ++f) {
-    v4f p[RT][NT], sum[RT];
-#pragma unroll
-    for (int m = 0; m < RT; ++m) {
-      sum[m] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < NT; ++s) p[m][s] = v4f{0.f, 0.f, 0.f, 0.f};
-    }
-#pragma unroll
-    for (int i = 0; i < FOLD; ++i) {
-      const int j = f * FOLD + i;
-      __builtin_amdgcn_sched_barrier(0);  // one step's values in registers at a time
-      u32x4 w[NT];
-#pragma unroll
-      for (int s = 0; s < NT; ++s) w[s] = widen<XT, FMT>(t.q[s][j]);
-#pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        const u32x4 v = x(m, j);
-#pragma unroll
-        for (int s = 0; s < NT; ++s) p[m][s] = mfma(XT{}, v, w[s], p[m][s]);
-        if constexpr (FMT == kInt4) sum[m] = mfma(XT{}, v, ones<XT>(), sum[m]);
-      }
-    }
-#pragma unroll
-    for (int s = 0; s < NT; ++s) {
-      const float scale = scale_value<SIZE>(t.s[s].get(f), g.scale_dtype);
-      const float z = FMT != kInt4 ? 0.f : g.zeros != nullptr ? -(float)t.z[s].get(f) : -8.f;
-#pragma unroll
-      for (int m = 0; m < RT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = FMT == kInt4 ? fmaf(z, sum[m][i], p[m][s][i]) : p[m][s][i];
-          acc[m][s][i] = fmaf(scale, v, acc[m][s][i]);
-        }
-    }
-  }
-}
 
 __device__ __forceinline__ void store(const W4GemmArgs& g, float v, long long r, int n) {
   const long long at = r * g.c_stride + n;
@@ -303,10 +414,10 @@ __device__ __forceinline__ void store(const W4GemmArgs& g, float v, long long r,
 }
 
 // result (r, n) by the definition; brow: its weight row, of all experts' rows
-template <typename XT>
+template <typename XT, int FMT>
 __device__ __noinline__ void plain_result(W4GemmArgs g, int r, int n, long long brow) {
   const auto sum = [&](long long row) {
-    return plain_sum(static_cast<const XT*>(g.A) + r * g.a_stride, g.B + row * (g.K / 2), g.scales, g.zeros,
+    return plain_sum<XT, FMT>(static_cast<const XT*>(g.A) + r * g.a_stride, g.B + row * (g.K / 2), g.scales, g.zeros,
                      row * (g.K / g.G), g.K, g.G, g.scale_dtype);
   };
   const float v = sum(brow);
@@ -329,19 +440,18 @@ __device__ __forceinline__ void finish(const W4GemmArgs& g, const v4f (&acc)[RT]
       if (r >= m_end) continue;
 #pragma unroll
       for (int s = 0; s < NT; ++s) good = good && finite(acc[m][s][i]);
-      if (g.act >= 0) {
-        if (c.n0 + r16 < g.N) store(g, activate(g, acc[m][0][i], acc[m][NT - 1][i]), r, c.n0 + r16);
-      } else {
 #pragma unroll
-        for (int s = 0; s < NT; ++s)
-          if (c.n0 + s * 16 + r16 < g.N) store(g, acc[m][s][i], r, c.n0 + s * 16 + r16);
+      for (int s = 0; s < NT; ++s) {
+        const int n = c.n0 + s * 16 + r16;
+        if (n >= g.N || (g.act >= 0 && s >= NT / 2)) continue;
+        store(g, g.act >= 0 ? activate(g, acc[m][s][i], acc[m][s < NT / 2 ? s + NT / 2 : s][i]) : acc[m][s][i], r, n);
       }
     }
-  if (FMT == kInt4 && !good)
-    for (int s = 0; s < (g.act >= 0 ? 1 : NT); ++s)
+  if (!good)
+    for (int s = 0; s < (g.act >= 0 ? NT / 2 : NT); ++s)
       for (int i = 0; i < RT * 4; ++i) {
         const int r = m0 + i / 4 * 16 + 4 * q4 + i % 4, n = c.n0 + s * 16 + r16;
-        if (r < m_end && n < g.N) plain_result<XT>(g, r, n, c.first[0] + s * 16 + r16);
+        if (r < m_end && n < g.N) plain_result<XT, FMT>(g, r, n, c.first[0] + s * 16 + r16);
       }
 }
 
@@ -355,7 +465,7 @@ template <typename XT, int FMT, int SIZE, int FOLD, int NT, int WK>
 __global__ __launch_bounds__(WK == 1 ? 256 : WK * 64, 4) void w4_few_kernel(W4GemmArgs g, uint64_t per_group) {
   __shared__ float part[WK > 1 ? WK : 1][16][NT * 16 + 1];
   const int lane = threadIdx.x & 63, r16 = lane & 15, q4 = lane >> 4, wave = wave_id();
-  const int e = blockIdx.y, cols = g.act >= 0 ? 16 : NT * 16;
+  const int e = blockIdx.y, cols = g.act >= 0 ? NT * 8 : NT * 16;
   const int2 rr = expert_rows(g.offsets, e, g.rows);
   const long long column = (long long)(WK == 1 ? blockIdx.x * 4 + wave : blockIdx.x) * cols;
   if (column >= g.N || rr.x >= rr.y) return;
@@ -375,11 +485,11 @@ __global__ __launch_bounds__(WK == 1 ? 256 : WK * 64, 4) void w4_few_kernel(W4Ge
 #pragma unroll
       for (int j = 0; j < 4; ++j) k.x[j] = load_row16(xb + (FOLD == 4 ? j * 16 : j * 64));
     };
-    v4f acc[1][NT];
-#pragma unroll
-    for (int s = 0; s < NT; ++s) acc[0][s] = v4f{0.f, 0.f, 0.f, 0.f};
+    Sums<FMT, 1, NT> sums;
+    sums.clear();
     const auto mul = [&](Block& k) {
-      multiply<XT, FMT, SIZE, FOLD, 1, NT>(g, k.t, [&](int, int j) { return k.x[j]; }, acc);
+      u32x4 v[1] = {k.x[0]};
+      k.t.template multiply_into<XT>(g, v, [&](int, int j) { return k.x[j & 3]; }, sums);
     };
     // two blocks in turn, the next one's loads in flight; none of them under a condition, which would make the wait for
     // one block's a wait for all
@@ -407,6 +517,8 @@ __global__ __launch_bounds__(WK == 1 ? 256 : WK * 64, 4) void w4_few_kernel(W4Ge
       }
       mul(b0);
     }
+    sums.finish();
+    const auto& acc = sums.acc;
     if constexpr (WK == 1) {
       finish<XT, FMT>(g, acc, c, m0, rr.y);
     } else {
@@ -426,8 +538,8 @@ __global__ __launch_bounds__(WK == 1 ? 256 : WK * 64, 4) void w4_few_kernel(W4Ge
         const int r = i / cols, col = i % cols;
         if (c.n0 + col >= g.N) continue;
         float v = total(r, col), up = 0.f;
-        if (g.act >= 0) up = total(r, NT * 16 - 16 + col);
-        if (FMT == kInt4 && !(finite(v) && finite(up))) plain_result<XT>(g, m0 + r, c.n0 + col, c.first[0] + col);
+        if (g.act >= 0) up = total(r, NT * 8 + col);
+        if (!(finite(v) && finite(up))) plain_result<XT, FMT>(g, m0 + r, c.n0 + col, c.first[0] + col);
         else store(g, g.act >= 0 ? activate(g, v, up) : v, m0 + r, c.n0 + col);
       }
       __syncthreads();
@@ -435,75 +547,267 @@ __global__ __launch_bounds__(WK == 1 ? 256 : WK * 64, 4) void w4_few_kernel(W4Ge
   }
 }
 
-// Up to 64 rows at a time: a workgroup of four waves, 32 weight rows each, the rows' values brought to LDS by all four, 128 of
-// K at a time into one of two slots.
+// The scales and zero points of a wave's weight rows, 64 groups at a time: each quarter of the lanes loads 16 consecutive ones of its
+// row, whole cache lines between them, and the wave's own part of LDS gives them out as they are needed.  (Loaded in place, a few
+// bytes of each row at a time, they took 15 of 132 us.)  FOLD: 1, 2, 4 or, for groups of more than 128, 8
+template <int FMT, int SIZE, int NT>
+struct ScaleLoad {
+  Items<16, SIZE> s[NT];
+  Items<16, 1> z[NT];
+
+  __device__ __forceinline__ void load(const W4GemmArgs& g, const Columns<SIZE, NT>& c, int u) {
+    const int ng = g.K / g.G, q4 = (threadIdx.x >> 4) & 3, have = ng - u * 64 - q4 * 16;
+    const bool full = u * 64 + 64 <= ng;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const gptr sp = scalar(c.s[t] + u * 64 * SIZE) + vector(c.s_off[t] + q4 * 16 * SIZE);
+      const gptr zp = scalar(c.z[t] + u * 64 * c.z_mul) + vector(c.z_off[t] + q4 * 16 * c.z_mul);
+      if (full) s[t].load(sp);
+      else s[t].load_first(sp, have);
+      if constexpr (FMT == kInt4) {
+        if (full) z[t].load(zp);
+        else if (g.zeros != nullptr) z[t].load_first(zp, have);
+      }
+    }
+  }
+};
+template <int FMT, int SIZE, int NT>
+struct ScaleLds {
+  // a row's 64 items and a few bytes, so that 16 rows' equal ones lie in different banks
+  static constexpr int kS = 64 * SIZE + (SIZE == 1 ? 4 : 8), kZ = FMT == kInt4 ? 64 + 4 : 0, kBytes = NT * 16 * (kS + kZ);
+  uint8_t* at;  // this lane's row
+
+  __device__ __forceinline__ uint8_t* scales(int t) const { return at + t * 16 * kS; }
+  __device__ __forceinline__ uint8_t* zeros(int t) const { return at + NT * 16 * kS + t * 16 * kZ - (threadIdx.x & 15) * (kS - kZ); }
+  __device__ __forceinline__ void put(const ScaleLoad<FMT, SIZE, NT>& l) const {
+    const int q4 = (threadIdx.x >> 4) & 3;
+    typedef uint32_t word __attribute__((aligned(4)));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int i = 0; i < Items<16, SIZE>::kWords; ++i) reinterpret_cast<word*>(scales(t) + q4 * 16 * SIZE)[i] = l.s[t].w[i];
+      if constexpr (FMT == kInt4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) reinterpret_cast<word*>(zeros(t) + q4 * 16)[i] = l.z[t].w[i];
+      }
+    }
+  }
+};
+
+// At most 16 rows at a time by many weight rows: a workgroup of four waves, 16 NT weight rows each.  The rows' values go through
+// LDS, 16 KB of them at a time into one of two slots; the codes come from memory 512 of K ahead.  grid (column tiles, experts, row
+// tiles)
+template <typename XT, int FMT, int SIZE, int FOLD, int NT>
+__global__ __launch_bounds__(256, STREAM_OCC) void w4_stream_kernel(W4GemmArgs g, uint64_t per_group) {
+  constexpr int F = FOLD > 4 ? 4 : FOLD, NS = 4 / F, kSlot = 16384;  // NS: scales of a block of 128
+  using Lds = ScaleLds<FMT, SIZE, NT>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][kSlot];
+  __shared__ __attribute__((aligned(16))) uint8_t scale_lds[4][Lds::kBytes];
+  const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, q4 = lane >> 4;
+  const int e = blockIdx.y, cols = g.act >= 0 ? 8 * NT : 16 * NT;
+  const int2 rr = expert_rows(g.offsets, e, g.rows);
+  const long long column = (long long)(blockIdx.x * 4 + wave_id()) * cols;
+  const bool mine = column < g.N;  // a wave without columns helps with the rows
+  Columns<SIZE, NT> c;
+  c.init(g, e, mine ? (int)column : 0);
+  const Lds sl{scale_lds[wave_id()] + r16 * Lds::kS};
+  const int nfull = g.K / 512, nsb = (g.K + 511) / 512, nblk = (g.K + 127) / 128, ng = g.K / g.G;
+  for (long long m = rr.x + (long long)blockIdx.z * 16; m < rr.y; m += (long long)gridDim.z * 16) {
+    const int m0 = (int)m, rows = min(16, rr.y - m0);
+    // a slot holds 16 KB / rows (rounded up to a power of two) of each row
+    const int row_log2 = rows <= 1 ? 0 : 32 - __builtin_clz(rows - 1);
+    const int sb_log2 = 4 - row_log2, nslots = (nsb + (1 << sb_log2) - 1) >> sb_log2;
+    // thread: 16-byte chunk at[i] of a row's part of a slot
+    const XT* src[4];
+    int at[4], to[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int id = tid + 256 * i, row = id >> (6 + sb_log2);
+      at[i] = (id & ((64 << sb_log2) - 1)) * 8;
+      src[i] = static_cast<const XT*>(g.A) + (long long)(m0 + min(row, rows - 1)) * g.a_stride;
+      to[i] = (id ^ (row & 7)) * 16;
+    }
+    u32x4 stage[4];
+    const auto fetch = [&](int slot) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = (slot << sb_log2) * 512 + at[i];
+        stage[i] = load_row16(vector(src[i] + min(k, g.K - 8)));
+        if (k >= g.K) stage[i] = u32x4{0, 0, 0, 0};
+      }
+    };
+    const auto put = [&](int slot) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4*>(lds[slot & 1] + to[i]) = turn<FMT>(stage[i]);
+    };
+    // where a lane's values of step j lie in a block: the low three bits of a chunk's number are turned by the row's
+    const int xrow = min(r16, rows - 1);
+    int xoff[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      xoff[j] = (xrow << (10 + sb_log2)) + (((F == 4 ? q4 * 4 + j : j * 4 + q4) ^ (xrow & 7)) * 16);
+    Sums<FMT, 1, NT> sums;
+    sums.clear();
+    u32x4 q[4][NT], xv[1];
+    ScaleLoad<FMT, SIZE, NT> sc;
+    const auto codes = [&](int b, u32x4 (&v)[NT]) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        v[t] = *(const MOE_GLOBAL u32x4*)(scalar(c.q[t] + (long long)b * 64) + vector(c.q_off[t]));
+    };
+    const auto group_of = [&](int b) { return FOLD > 4 ? (int)((uint32_t)b * per_group >> 32) : b * NS; };
+    // block i of the 512 of K at sb
+    const auto block = [&](int slot, int sb, int i) {
+      const uint8_t* base = lds[slot & 1] + (sb & ((1 << sb_log2) - 1)) * 1024;
+      const auto x = [&](int, int j) {  // past the 512 (not used, but in the slot) the first ones
+        return *reinterpret_cast<const u32x4*>(base + xoff[j & 3] + ((i + j / 4) & 3) * 256);
+      };
+      if (i == 0) xv[0] = x(0, 0);
+      Items<NS, SIZE> s[NT];
+      Items<NS, 1> z[NT];
+      const int at = group_of(sb * 4 + i) & 63;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        s[t].load_lds(sl.scales(t) + at * SIZE);
+        if constexpr (FMT == kInt4) z[t].load_lds(sl.zeros(t) + at);
+      }
+      multiply<XT, FMT, true, F, 1, NT>(
+          q[i], xv, x, [&](int t, int f) { return scale_value<SIZE>(s[t].get(f), g.scale_dtype); },
+          [&](int t, int f) { return g.zeros != nullptr ? (float)z[t].get(f) : 8.f; }, sums);
+    };
+    // the scales where the 512 of K at sb are the first that need them, and the next ones' loads
+    int unit = 0;
+    const auto turn_scales = [&](int sb) {
+      if (group_of(sb * 4) >> 6 == unit) {
+        sl.put(sc);
+        ++unit;
+        if (unit * 64 < ng) sc.load(g, c, unit);
+      }
+    };
+    fetch(0);
+    sc.load(g, c, 0);
+    if (nfull > 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) codes(i, q[i]);
+    }
+    put(0);
+    for (int slot = 0, sb = 0; slot < nslots; ++slot) {
+      __syncthreads();  // this slot is written, and the other one's readers are done
+      fetch(min(slot + 1, nslots - 1));
+      const int end = min((slot + 1) << sb_log2, nfull);
+      for (; sb < end; ++sb) {
+        turn_scales(sb);
+        const int next = min(sb + 1, nfull - 1);  // past the end the last ones again, so that no load of codes is under a condition
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          block(slot, sb, i);
+          codes(next * 4 + i, q[i]);
+        }
+      }
+      if (slot == nslots - 1 && nfull < nsb) {  // less than 512 at the end
+        turn_scales(nfull);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            q[i][t] = u32x4{0, 0, 0, 0};
+            if (nfull * 512 + i * 128 + q4 * 32 < g.K) q[i][t] = *reinterpret_cast<const u32x4*>(c.q[t] + (nfull * 4 + i) * 64LL + c.q_off[t]);
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (nfull * 4 + i < nblk) block(slot, nfull, i);
+      }
+      put(slot + 1);
+    }
+    sums.finish();
+    if (mine) finish<XT, FMT>(g, sums.acc, c, m0, rr.y);
+    __syncthreads();
+  }
+}
+
+// Up to 64 rows at a time: a workgroup of four waves, 32 weight rows each.  The rows' values are brought to LDS by all four, 256
+// of K at a time into one of two slots; the codes come two blocks of 128 ahead.
 template <typename XT, int FMT, int SIZE, int FOLD, int RT>
-__device__ __forceinline__ void tile_rows(const W4GemmArgs& g, uint64_t per_group, uint8_t (*lds)[64 * 256],
+__device__ __forceinline__ void tile_rows(const W4GemmArgs& g, uint64_t per_group, uint8_t (*lds)[64 * 512],
                                           const Columns<SIZE, 2>& c, bool mine, int m0, int m_end) {
   const int lane = threadIdx.x & 63, r16 = lane & 15, q4 = lane >> 4, tid = threadIdx.x;
-  const int nfull = g.K / 128;
-  // thread: 16-byte chunk tid % 16 of rows tid / 16 + 16 m; in LDS a row's chunks are turned by its number, so that 16 rows' equal
-  // chunks lie in different banks
+  const int nfull = g.K / 128, nblk = (g.K + 127) / 128;
+  // thread: 16-byte chunk tid % 16 of a block of rows tid / 16 + 16 m; the low four bits of a chunk's number are turned by the
+  // row's, so that 16 rows' equal chunks lie in different banks
   const int srow = tid >> 4, chunk = tid & 15;
   const XT* src[RT];
 #pragma unroll
   for (int m = 0; m < RT; ++m)
     src[m] = static_cast<const XT*>(g.A) + (long long)min(m0 + m * 16 + srow, m_end - 1) * g.a_stride + chunk * 8;
   u32x4 stage[RT];
-  Codes<FMT, SIZE, FOLD, 2> next;
+  // the rows' values of block b, zero past K
   const auto fetch = [&](int b) {
-#pragma unroll
-    for (int m = 0; m < RT; ++m) stage[m] = load_row16(vector(src[m] + b * 128));
-    next.template load<true>(g, c, b, per_group);
-  };
-  const auto put = [&](int b) {
-#pragma unroll
-    for (int m = 0; m < RT; ++m)
-      *reinterpret_cast<u32x4*>(lds[b & 1] + (m * 16 + srow) * 256 + ((chunk ^ srow) & 15) * 16) = stage[m];
-  };
-  v4f acc[RT][2];
-#pragma unroll
-  for (int m = 0; m < RT; ++m)
-#pragma unroll
-    for (int s = 0; s < 2; ++s) acc[m][s] = v4f{0.f, 0.f, 0.f, 0.f};
-  const auto step = [&](int b, Codes<FMT, SIZE, FOLD, 2>& codes) {
-    const uint8_t* at = lds[b & 1] + r16 * 256;
-    multiply<XT, FMT, SIZE, FOLD, RT, 2>(g, codes, [&](int m, int j) {
-      const int k = FOLD == 4 ? q4 * 4 + j : j * 4 + q4;
-      return *reinterpret_cast<const u32x4*>(at + m * 16 * 256 + (k ^ r16) * 16);
-    }, acc);
-  };
-  if (nfull > 0) {
-    fetch(0);
-    put(0);
-    for (int b = 0; b + 1 < nfull; ++b) {
-      __syncthreads();  // this block's slot is written, and the other one's readers are done
-      Codes<FMT, SIZE, FOLD, 2> now = next;
-      fetch(b + 1);
-      step(b, now);
-      put(b + 1);
-    }
-    __syncthreads();
-    step(nfull - 1, next);
-  }
-  if (FOLD < 4 && nfull * 128 < g.K) {  // the last, partial block
+    const bool in = FOLD == 4 || b * 128 + chunk * 8 < g.K;
 #pragma unroll
     for (int m = 0; m < RT; ++m) {
-      stage[m] = u32x4{0, 0, 0, 0};
-      if (nfull * 128 + chunk * 8 < g.K) stage[m] = load16(src[m] + nfull * 128);
+      stage[m] = load_row16(vector(src[m] + (in ? b * 128 : 0)));
+      if (!in) stage[m] = u32x4{0, 0, 0, 0};
     }
-    next.template load<false>(g, c, nfull, per_group);
-    put(nfull);
-    __syncthreads();
-    step(nfull, next);
+  };
+  const auto put = [&](int b) {
+    uint8_t* at = lds[(b >> 1) & 1] + (b & 1) * 256 + srow * 512 + ((chunk ^ srow) & 15) * 16;
+#pragma unroll
+    for (int m = 0; m < RT; ++m) *reinterpret_cast<u32x4*>(at + m * 16 * 512) = stage[m];
+  };
+  int xoff[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) xoff[j] = r16 * 512 + (((FOLD == 4 ? q4 * 4 + j : j * 4 + q4) ^ r16) * 16);
+  Sums<FMT, RT, 2> sums;
+  sums.clear();
+  const auto step = [&](int b, Codes<FMT, SIZE, FOLD, 2>& codes) {
+    const uint8_t* at = lds[(b >> 1) & 1] + (b & 1) * 256;
+    const auto x = [&](int m, int j) { return *reinterpret_cast<const u32x4*>(at + m * 16 * 512 + xoff[j & 3]); };
+    u32x4 v[RT];
+#pragma unroll
+    for (int m = 0; m < RT; ++m) v[m] = x(m, 0);
+    codes.template multiply_into<XT>(g, v, x, sums);
+  };
+  // Blocks go in pairs, a slot each; a last odd or partial one is read with its conditions.  No load is under a condition
+  // before that: past the last pair the same one is read again
+  const int npairs = nfull / 2;
+  Codes<FMT, SIZE, FOLD, 2> c0, c1;
+  fetch(0);
+  put(0);
+  if (nblk > 1) {
+    fetch(1);
+    put(1);
   }
-  if (mine) finish<XT, FMT>(g, acc, c, m0, m_end);
+  if (npairs > 0) {
+    c0.template load<true>(g, c, 0, per_group);
+    c1.template load<true>(g, c, 1, per_group);
+  }
+  for (int p = 0; p < npairs; ++p) {
+    __syncthreads();  // this slot is written, and the other one's readers are done
+    const int to = min(p + 1, npairs - 1) * 2, xto = min(2 * p + 2, nblk - 1);
+    fetch(xto);
+    step(2 * p, c0);
+    c0.template load<true>(g, c, to, per_group);
+    put(2 * p + 2);
+    fetch(min(xto + 1, nblk - 1));
+    step(2 * p + 1, c1);
+    c1.template load<true>(g, c, to + 1, per_group);
+    put(2 * p + 3);
+  }
+  if (npairs * 2 < nblk) {
+    __syncthreads();
+    for (int b = npairs * 2; b < nblk; ++b) {
+      c0.template load<false>(g, c, b, per_group);
+      step(b, c0);
+    }
+  }
+  sums.finish();
+  if (mine) finish<XT, FMT>(g, sums.acc, c, m0, m_end);
   __syncthreads();
 }
 
 template <typename XT, int FMT, int SIZE, int FOLD>
 __global__ __launch_bounds__(256, 2) void w4_tile_kernel(W4GemmArgs g, uint64_t per_group) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][64 * 256];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][64 * 512];
   const int e = blockIdx.y, cols = g.act >= 0 ? 16 : 32;
   const int2 rr = expert_rows(g.offsets, e, g.rows);
   const long long column = (long long)(blockIdx.x * 4 + wave_id()) * cols;
@@ -528,19 +832,21 @@ hipError_t launch(const W4GemmArgs& g, hipStream_t s) {
     return hipGetLastError();
   };
   const bool act = g.act >= 0;
-  if (g.rows > 16 && g.rows > 8LL * g.groups) return go(w4_tile_kernel<XT, FMT, SIZE, FOLD>, act ? 64 : 128, 256, 64);
+  constexpr int F = FOLD > 4 ? 4 : FOLD;
+  if (g.rows > 16 && g.rows > 8LL * g.groups) return go(w4_tile_kernel<XT, FMT, SIZE, F>, act ? 64 : 128, 256, 64);
   // tiles of 32 weight rows; while they fill the GPU's waves, one wave for each
   const long long tiles = (long long)g.groups * ((g.N + 15) / 16) * (act ? 2 : 1) / 2;
-  if (tiles >= 2048) return go(w4_few_kernel<XT, FMT, SIZE, FOLD, 2, 4>, act ? 16 : 32, 256, 16);
-  if (act || tiles >= 512) return go(w4_few_kernel<XT, FMT, SIZE, FOLD, 2, 8>, act ? 16 : 32, 512, 16);
-  return go(w4_few_kernel<XT, FMT, SIZE, FOLD, 1, 16>, 16, 1024, 16);
+  if (tiles >= 256) return go(w4_stream_kernel<XT, FMT, SIZE, FOLD, STREAM_NT>, act ? 32 * STREAM_NT : 64 * STREAM_NT, 256, 16);
+  if (act || tiles >= 512) return go(w4_few_kernel<XT, FMT, SIZE, F, 2, 8>, act ? 16 : 32, 512, 16);
+  return go(w4_few_kernel<XT, FMT, SIZE, F, 1, 16>, 16, 1024, 16);
 }
 
 template <typename XT, int SIZE>
 hipError_t int4_by_group(const W4GemmArgs& g, hipStream_t s) {
   if (g.G == 32) return launch<XT, kInt4, SIZE, 1>(g, s);
   if (g.G == 64) return launch<XT, kInt4, SIZE, 2>(g, s);
-  return launch<XT, kInt4, SIZE, 4>(g, s);
+  if (g.G == 128) return launch<XT, kInt4, SIZE, 4>(g, s);
+  return launch<XT, kInt4, SIZE, 8>(g, s);
 }
 template <typename XT>
 hipError_t by_weights(const W4GemmArgs& g, bool mxfp4, hipStream_t s) {
