@@ -20,12 +20,6 @@
 #include "elem.hpp"
 #include "operators.hpp"
 
-#ifndef STREAM_OCC
-#define STREAM_OCC 2
-#endif
-#ifndef STREAM_NT
-#define STREAM_NT 2
-#endif
 namespace moe {
 
 namespace {
@@ -179,19 +173,6 @@ struct Items {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
   }
-  // whole ones of 4 items as far as there are `have`, and the rest one by one
-  __device__ __forceinline__ void load_first(gptr p, int have) {
-    if constexpr (N > 4) {
-#pragma unroll
-      for (int i = 0; i < N / 4; ++i) {
-        Items<4, SIZE> q = {};
-        if (have >= 4 * i + 4) q.load(p + 4 * SIZE * i);
-        else if (have > 4 * i) q.load(p + 4 * SIZE * i, have - 4 * i);
-#pragma unroll
-        for (int j = 0; j < SIZE; ++j) w[i * SIZE + j] = q.w[j];
-      }
-    }
-  }
   __device__ __forceinline__ uint32_t get(int i) const {
     if constexpr (SIZE == 4) return w[i];
     else if constexpr (SIZE == 2) return (w[i >> 1] >> (16 * (i & 1))) & 0xffffu;
@@ -339,7 +320,10 @@ __device__ __forceinline__ void multiply(u32x4 (&q)[NT], u32x4 (&v)[RT], X x, S 
 #pragma unroll
       for (int m = 0; m < RT; ++m) ahead[m] = x(m, j + 1);
 #pragma unroll
-      for (int s = 0; s < NT; ++s) w[s] = widen<XT, FMT, TURNED>(q[s][j]);
+      for (int s = 0; s < NT; ++s) {
+        w[s] = widen<XT, FMT, TURNED>(q[s][j]);
+        if constexpr (RT > 1) asm("" : "+v"(w[s]));  // once for all rows' tiles: the compiler widens again for each
+      }
 #pragma unroll
       for (int m = 0; m < RT; ++m) {
 #pragma unroll
@@ -370,41 +354,6 @@ __device__ __forceinline__ void multiply(u32x4 (&q)[NT], u32x4 (&v)[RT], X x, S 
     }
   }
 }
-
-// What a wave needs of the weights for 128 of K.  FOLD: 32-wide steps that go under one scale; SIZE: a scale's bytes
-template <int FMT, int SIZE, int FOLD, int NT>
-struct Codes {
-  static constexpr int NS = 4 / FOLD;  // scales
-  u32x4 q[NT];
-  Items<NS, SIZE> s[NT];
-  Items<NS, 1> z[NT];
-
-  // block b of K; FULL: all 128 are there.  per_group: 2^32 over the blocks of a group, rounded up
-  template <bool FULL>
-  __device__ __forceinline__ void load(const W4GemmArgs& g, const Columns<SIZE, NT>& c, int b, uint64_t per_group) {
-    const int g0 = FOLD < 4 ? b * NS : (int)((uint32_t)b * per_group >> 32);
-    const int have = g.K / g.G - g0, q4 = (threadIdx.x >> 4) & 3;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      q[i] = u32x4{0, 0, 0, 0};
-      if (FULL || b * 128 + q4 * 32 < g.K) q[i] = *(const MOE_GLOBAL u32x4*)(scalar(c.q[i] + (long long)b * 64) + vector(c.q_off[i]));
-      const gptr sp = scalar(c.s[i] + g0 * SIZE) + vector(c.s_off[i]);
-      const gptr zp = scalar(c.z[i] + g0 * c.z_mul) + vector(c.z_off[i]);
-      if constexpr (FULL) s[i].load(sp);
-      else s[i].load(sp, have);
-      if constexpr (FMT == kInt4) {
-        if constexpr (FULL) z[i].load(zp);
-        else z[i].load(zp, have);
-      }
-    }
-  }
-  template <typename XT, int RT, typename X>
-  __device__ __forceinline__ void multiply_into(const W4GemmArgs& g, u32x4 (&v)[RT], X x, Sums<FMT, RT, NT>& sums) {
-    multiply<XT, FMT, false, FOLD, RT, NT>(
-        q, v, x, [&](int t, int f) { return scale_value<SIZE>(s[t].get(f), g.scale_dtype); },
-        [&](int t, int f) { return g.zeros != nullptr ? (float)z[t].get(f) : 8.f; }, sums);
-  }
-};
 
 __device__ __forceinline__ void store(const W4GemmArgs& g, float v, long long r, int n) {
   const long long at = r * g.c_stride + n;
@@ -457,150 +406,231 @@ __device__ __forceinline__ void finish(const W4GemmArgs& g, const v4f (&acc)[RT]
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-// At most 16 rows at a time.  WK = 1: a workgroup of four waves, each with its own 16 NT weight rows; WK > 1: the WK waves
-// share theirs, each takes every WK-th 128 of K, and their sums meet in LDS, in wave order.  The rows' values come straight from
-// the caches; lanes past the last row read that one, and their results are not stored.  grid (column tiles, experts, row
-// tiles)
-template <typename XT, int FMT, int SIZE, int FOLD, int NT, int WK>
-__global__ __launch_bounds__(WK == 1 ? 256 : WK * 64, 4) void w4_few_kernel(W4GemmArgs g, uint64_t per_group) {
-  __shared__ float part[WK > 1 ? WK : 1][16][NT * 16 + 1];
-  const int lane = threadIdx.x & 63, r16 = lane & 15, q4 = lane >> 4, wave = wave_id();
-  const int e = blockIdx.y, cols = g.act >= 0 ? NT * 8 : NT * 16;
-  const int2 rr = expert_rows(g.offsets, e, g.rows);
-  const long long column = (long long)(WK == 1 ? blockIdx.x * 4 + wave : blockIdx.x) * cols;
-  if (column >= g.N || rr.x >= rr.y) return;
-  Columns<SIZE, NT> c;
-  c.init(g, e, (int)column);
-  const int nfull = g.K / 128;
-  for (long long m = rr.x + (long long)blockIdx.z * 16; m < rr.y; m += (long long)gridDim.z * 16) {
-    const int m0 = (int)m;
-    const XT* xp = static_cast<const XT*>(g.A) + (long long)min(m0 + r16, rr.y - 1) * g.a_stride + (FOLD == 4 ? q4 * 32 : q4 * 8);
-    struct Block {
-      Codes<FMT, SIZE, FOLD, NT> t;
-      u32x4 x[4];
-    } b0, b1;
-    const auto load = [&](int b, Block& k) {
-      k.t.template load<true>(g, c, b, per_group);
-      const gptr xb = vector(xp + b * 128);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) k.x[j] = load_row16(xb + (FOLD == 4 ? j * 16 : j * 64));
-    };
-    Sums<FMT, 1, NT> sums;
-    sums.clear();
-    const auto mul = [&](Block& k) {
-      u32x4 v[1] = {k.x[0]};
-      k.t.template multiply_into<XT>(g, v, [&](int, int j) { return k.x[j & 3]; }, sums);
-    };
-    // two blocks in turn, the next one's loads in flight; none of them under a condition, which would make the wait for
-    // one block's a wait for all
-    int b = WK > 1 ? wave : 0;
-    if (b < nfull) load(b, b0);
-    for (; b + 2 * WK < nfull; b += 2 * WK) {
-      load(b + WK, b1);
-      mul(b0);
-      load(b + 2 * WK, b0);
-      mul(b1);
-    }
-    if (b + WK < nfull) {
-      load(b + WK, b1);
-      mul(b0);
-      mul(b1);
-    } else if (b < nfull) {
-      mul(b0);
-    }
-    if (FOLD < 4 && nfull * 128 < g.K && (WK == 1 || nfull % WK == wave)) {
-      b0.t.template load<false>(g, c, nfull, per_group);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        b0.x[j] = u32x4{0, 0, 0, 0};
-        if (nfull * 128 + j * 32 < g.K) b0.x[j] = load16(xp + nfull * 128 + j * 32);
-      }
-      mul(b0);
-    }
-    sums.finish();
-    const auto& acc = sums.acc;
-    if constexpr (WK == 1) {
-      finish<XT, FMT>(g, acc, c, m0, rr.y);
-    } else {
-#pragma unroll
-      for (int s = 0; s < NT; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[wave][4 * q4 + i][s * 16 + r16] = acc[0][s][i];
-      __syncthreads();
-      const int rows = min(16, rr.y - m0);
-      const auto total = [&](int r, int col) {
-        float v = part[0][r][col];
-#pragma unroll
-        for (int w = 1; w < WK; ++w) v += part[w][r][col];
-        return v;
-      };
-      for (int i = threadIdx.x; i < rows * cols; i += WK * 64) {
-        const int r = i / cols, col = i % cols;
-        if (c.n0 + col >= g.N) continue;
-        float v = total(r, col), up = 0.f;
-        if (g.act >= 0) up = total(r, NT * 8 + col);
-        if (!(finite(v) && finite(up))) plain_result<XT, FMT>(g, m0 + r, c.n0 + col, c.first[0] + col);
-        else store(g, g.act >= 0 ? activate(g, v, up) : v, m0 + r, c.n0 + col);
-      }
-      __syncthreads();
-    }
-  }
-}
-
-// The scales and zero points of a wave's weight rows, 64 groups at a time: each quarter of the lanes loads 16 consecutive ones of its
-// row, whole cache lines between them, and the wave's own part of LDS gives them out as they are needed.  (Loaded in place, a few
-// bytes of each row at a time, they took 15 of 132 us.)  FOLD: 1, 2, 4 or, for groups of more than 128, 8
-template <int FMT, int SIZE, int NT>
+// The scales and zero points of a wave's weight rows, kUnit groups at a time: each quarter of the lanes loads a quarter of them of its
+// row, runs of 64 bytes and more between them, and the wave's own part of LDS gives them out as they are needed.  (Loaded in
+// place, a few bytes of each row at a time, they took 15 of 132 us.)  Rows whose number of groups is no multiple of four are
+// copied item by item.
+template <int FMT, int SIZE, int NT, int kUnit>
 struct ScaleLoad {
-  Items<16, SIZE> s[NT];
-  Items<16, 1> z[NT];
+  static constexpr int kPart = kUnit / 4;
+  Items<kPart, SIZE> s[NT];
+  Items<kPart, 1> z[NT];
 
-  __device__ __forceinline__ void load(const W4GemmArgs& g, const Columns<SIZE, NT>& c, int u) {
-    const int ng = g.K / g.G, q4 = (threadIdx.x >> 4) & 3, have = ng - u * 64 - q4 * 16;
-    const bool full = u * 64 + 64 <= ng;
+  // groups past the row's last one are not used: the last ones again
+  __device__ __forceinline__ void load(const W4GemmArgs& g, const Columns<SIZE, NT>& c, int base) {
+    const int ng = g.K / g.G, first = base + ((threadIdx.x >> 4) & 3) * kPart;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const gptr sp = scalar(c.s[t] + u * 64 * SIZE) + vector(c.s_off[t] + q4 * 16 * SIZE);
-      const gptr zp = scalar(c.z[t] + u * 64 * c.z_mul) + vector(c.z_off[t] + q4 * 16 * c.z_mul);
-      if (full) s[t].load(sp);
-      else s[t].load_first(sp, have);
-      if constexpr (FMT == kInt4) {
-        if (full) z[t].load(zp);
-        else if (g.zeros != nullptr) z[t].load_first(zp, have);
+    for (int i = 0; i < kPart / 4; ++i) {
+      const uint32_t at = max(min(first + 4 * i, ng - 4), 0);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        Items<4, SIZE> v;
+        v.load(scalar(c.s[t]) + vector(c.s_off[t] + at * SIZE));
+#pragma unroll
+        for (int j = 0; j < SIZE; ++j) s[t].w[i * SIZE + j] = v.w[j];
+        if constexpr (FMT == kInt4) {
+          Items<4, 1> y;
+          y.load(scalar(c.z[t]) + vector(c.z_off[t] + at * c.z_mul));
+          z[t].w[i] = y.w[0];
+        }
       }
     }
   }
 };
-template <int FMT, int SIZE, int NT>
+template <int FMT, int SIZE, int NT, int kUnit>
 struct ScaleLds {
-  // a row's 64 items and a few bytes, so that 16 rows' equal ones lie in different banks
-  static constexpr int kS = 64 * SIZE + (SIZE == 1 ? 4 : 8), kZ = FMT == kInt4 ? 64 + 4 : 0, kBytes = NT * 16 * (kS + kZ);
+  // a row's items and a few bytes, so that 16 rows' equal ones lie in different banks
+  static constexpr int kPart = kUnit / 4;
+  static constexpr int kS = kUnit * SIZE + (SIZE == 1 ? 4 : 8), kZ = FMT == kInt4 ? kUnit + 4 : 0, kBytes = NT * 16 * (kS + kZ);
   uint8_t* at;  // this lane's row
 
   __device__ __forceinline__ uint8_t* scales(int t) const { return at + t * 16 * kS; }
   __device__ __forceinline__ uint8_t* zeros(int t) const { return at + NT * 16 * kS + t * 16 * kZ - (threadIdx.x & 15) * (kS - kZ); }
-  __device__ __forceinline__ void put(const ScaleLoad<FMT, SIZE, NT>& l) const {
+  __device__ __forceinline__ void put(const ScaleLoad<FMT, SIZE, NT, kUnit>& l) const {
     const int q4 = (threadIdx.x >> 4) & 3;
-    typedef uint32_t word __attribute__((aligned(4)));
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int i = 0; i < Items<16, SIZE>::kWords; ++i) reinterpret_cast<word*>(scales(t) + q4 * 16 * SIZE)[i] = l.s[t].w[i];
+      for (int i = 0; i < Items<kPart, SIZE>::kWords; ++i) reinterpret_cast<uint32_t*>(scales(t) + q4 * kPart * SIZE)[i] = l.s[t].w[i];
       if constexpr (FMT == kInt4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) reinterpret_cast<word*>(zeros(t) + q4 * 16)[i] = l.z[t].w[i];
+        for (int i = 0; i < kPart / 4; ++i) reinterpret_cast<uint32_t*>(zeros(t) + q4 * kPart)[i] = l.z[t].w[i];
+      }
+    }
+  }
+  __device__ __forceinline__ void copy(const W4GemmArgs& g, const Columns<SIZE, NT>& c, int base) const {
+    const int ng = g.K / g.G, q4 = (threadIdx.x >> 4) & 3;
+    for (int i = 0; i < kPart; ++i) {
+      const uint32_t at = min(base + q4 * kPart + i, ng - 1);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        Items<1, SIZE> v;
+        v.load(scalar(c.s[t]) + vector(c.s_off[t] + at * SIZE));
+        uint8_t* to = scales(t) + (q4 * kPart + i) * SIZE;
+        if constexpr (SIZE == 4) *reinterpret_cast<uint32_t*>(to) = v.w[0];
+        else if constexpr (SIZE == 2) *reinterpret_cast<uint16_t*>(to) = (uint16_t)v.w[0];
+        else *to = (uint8_t)v.w[0];
+        if constexpr (FMT == kInt4) {
+          Items<1, 1> y;
+          y.load(scalar(c.z[t]) + vector(c.z_off[t] + at * c.z_mul));
+          zeros(t)[q4 * kPart + i] = (uint8_t)y.w[0];
+        }
       }
     }
   }
 };
+
+// At most 16 rows at a time by 16 NT weight rows a workgroup: its WK waves share those, each takes a run of blocks of 128 of K, and their
+// sums meet in LDS, in wave order.
+//
+// What counts here is how many cache lines a load touches: a lane's part of the rows or of the scales, loaded where it is needed, touches
+// as many lines for a few bytes of each as its codes do.  So each wave brings scales and rows' values in longer runs, through
+// parts of LDS that are its own.  CH: 16-byte chunks of the rows' values that a lane brings, for 4 CH rows.
+template <typename XT, int FMT, int SIZE, int FOLD, int NT, int CH, typename Lds>
+__device__ __forceinline__ void few_rows(const W4GemmArgs& g, uint64_t per_group, const Columns<SIZE, NT>& c, const Lds& sl,
+                                         uint8_t* xl, int m0, int m_end, int first, int last, Sums<FMT, 1, NT>& sums) {
+  constexpr int F = FOLD > 4 ? 4 : FOLD, NS = 4 / F, kUnit = Lds::kPart * 4;  // NS: scales of a block
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q4 = lane >> 4;
+  const int ng = g.K / g.G;
+  // lane: chunk lane % 16 of rows lane / 16 + 4 i; a chunk's number is turned by the row's, so that 16 rows' equal chunks lie in
+  // different banks
+  const XT* src[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) src[i] = static_cast<const XT*>(g.A) + (long long)min(m0 + q4 + 4 * i, m_end - 1) * g.a_stride + r16 * 8;
+  const int xrow = min(r16, 4 * CH - 1);
+  int xoff[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) xoff[j] = xrow * 256 + (((F == 4 ? q4 * 4 + j : j * 4 + q4) ^ xrow) & 15) * 16;
+  struct Block {
+    u32x4 q[NT], x[CH];
+  } b0, b1;
+  const auto load = [&](int b, Block& k) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) k.q[t] = *(const MOE_GLOBAL u32x4*)(scalar(c.q[t] + (long long)b * 64) + vector(c.q_off[t]));
+#pragma unroll
+    for (int i = 0; i < CH; ++i) k.x[i] = load_row16(vector(src[i] + b * 128));
+  };
+  const auto group_of = [&](int b) { return FOLD > 4 ? (int)((uint32_t)b * per_group >> 32) : b * NS; };
+  int base = 0;  // first group in LDS
+  const auto mul = [&](int b, Block& k) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      *reinterpret_cast<u32x4*>(xl + (q4 + 4 * i) * 256 + ((r16 ^ (q4 + 4 * i)) & 15) * 16) = turn<FMT>(k.x[i]);
+    Items<NS, SIZE> s[NT];
+    Items<NS, 1> z[NT];
+    const int at = group_of(b) - base;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      s[t].load_lds(sl.scales(t) + at * SIZE);
+      if constexpr (FMT == kInt4) z[t].load_lds(sl.zeros(t) + at);
+    }
+    const auto x = [&](int, int j) { return *reinterpret_cast<const u32x4*>(xl + xoff[j & 3]); };
+    u32x4 xv[1] = {x(0, 0)};
+    multiply<XT, FMT, true, F, 1, NT>(
+        k.q, xv, x, [&](int t, int f) { return scale_value<SIZE>(s[t].get(f), g.scale_dtype); },
+        [&](int t, int f) { return g.zeros != nullptr ? (float)z[t].get(f) : 8.f; }, sums);
+  };
+  // as many blocks as kUnit - 4 groups make, or fewer, at a time
+  constexpr int kBlocks = (kUnit - 4) / NS;
+  for (int b = first; b < last;) {
+    const int end = min(b + kBlocks, last);
+    const bool full = end * 128 <= g.K;  // else the last block is partial
+    const int whole = full ? end : end - 1;
+    if (b < whole) load(b, b0);
+    base = group_of(b) & ~3;
+    if ((ng & 3) == 0) {
+      ScaleLoad<FMT, SIZE, NT, kUnit> sc;
+      sc.load(g, c, base);
+      sl.put(sc);
+    } else {
+      sl.copy(g, c, base);
+    }
+    // two blocks in turn, the next one's loads in flight; none of them under a condition, which would make the wait for
+    // one block's a wait for all
+    for (; b + 2 < whole; b += 2) {
+      load(b + 1, b1);
+      mul(b, b0);
+      load(b + 2, b0);
+      mul(b + 1, b1);
+    }
+    if (b + 1 < whole) {
+      load(b + 1, b1);
+      mul(b, b0);
+      mul(b + 1, b1);
+    } else if (b < whole) {
+      mul(b, b0);
+    }
+    if (FOLD < 4 && !full) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        b0.q[t] = u32x4{0, 0, 0, 0};
+        if (whole * 128 + q4 * 32 < g.K) b0.q[t] = *reinterpret_cast<const u32x4*>(c.q[t] + whole * 64LL + c.q_off[t]);
+      }
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        b0.x[i] = u32x4{0, 0, 0, 0};
+        if (whole * 128 + r16 * 8 < g.K) b0.x[i] = load16(src[i] + whole * 128);
+      }
+      mul(whole, b0);
+    }
+    b = end;
+  }
+}
+
+// grid (column tiles, experts, row tiles)
+template <typename XT, int FMT, int SIZE, int FOLD, int NT, int WK>
+__global__ __launch_bounds__(WK * 64, NT == 1 ? 3 : 2) void w4_few_kernel(W4GemmArgs g, uint64_t per_group) {
+  using Lds = ScaleLds<FMT, SIZE, NT, 32>;
+  __shared__ float part[WK][16][NT * 16 + 1];
+  __shared__ __attribute__((aligned(16))) uint8_t x_lds[WK][4096], scale_lds[WK][Lds::kBytes];
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q4 = lane >> 4, wave = wave_id();
+  const int e = blockIdx.y, cols = g.act >= 0 ? NT * 8 : NT * 16;
+  const int2 rr = expert_rows(g.offsets, e, g.rows);
+  if (rr.x >= rr.y) return;
+  Columns<SIZE, NT> c;
+  c.init(g, e, blockIdx.x * cols);
+  const Lds sl{scale_lds[wave] + r16 * Lds::kS};
+  // runs of blocks as even as they can be
+  const int nblk = (g.K + 127) / 128, first = (int)((long long)nblk * wave / WK), last = (int)((long long)nblk * (wave + 1) / WK);
+  for (long long m = rr.x + (long long)blockIdx.z * 16; m < rr.y; m += (long long)gridDim.z * 16) {
+    const int m0 = (int)m, rows = min(16, rr.y - m0);
+    Sums<FMT, 1, NT> sums;
+    sums.clear();
+    if (rows <= 4) few_rows<XT, FMT, SIZE, FOLD, NT, 1>(g, per_group, c, sl, x_lds[wave], m0, rr.y, first, last, sums);
+    else if (rows <= 8) few_rows<XT, FMT, SIZE, FOLD, NT, 2>(g, per_group, c, sl, x_lds[wave], m0, rr.y, first, last, sums);
+    else few_rows<XT, FMT, SIZE, FOLD, NT, 4>(g, per_group, c, sl, x_lds[wave], m0, rr.y, first, last, sums);
+    sums.finish();
+#pragma unroll
+    for (int s = 0; s < NT; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[wave][4 * q4 + i][s * 16 + r16] = sums.acc[0][s][i];
+    __syncthreads();
+    const auto total = [&](int r, int col) {
+      float v = part[0][r][col];
+#pragma unroll
+      for (int w = 1; w < WK; ++w) v += part[w][r][col];
+      return v;
+    };
+    for (int i = threadIdx.x; i < rows * cols; i += WK * 64) {
+      const int r = i / cols, col = i % cols;
+      if (c.n0 + col >= g.N) continue;
+      float v = total(r, col), up = 0.f;
+      if (g.act >= 0) up = total(r, NT * 8 + col);
+      if (!(finite(v) && finite(up))) plain_result<XT, FMT>(g, m0 + r, c.n0 + col, c.first[0] + col);
+      else store(g, g.act >= 0 ? activate(g, v, up) : v, m0 + r, c.n0 + col);
+    }
+    __syncthreads();
+  }
+}
 
 // At most 16 rows at a time by many weight rows: a workgroup of four waves, 16 NT weight rows each.  The rows' values go through
 // LDS, 16 KB of them at a time into one of two slots; the codes come from memory 512 of K ahead.  grid (column tiles, experts, row
 // tiles)
 template <typename XT, int FMT, int SIZE, int FOLD, int NT>
-__global__ __launch_bounds__(256, STREAM_OCC) void w4_stream_kernel(W4GemmArgs g, uint64_t per_group) {
+__global__ __launch_bounds__(256, 2) void w4_stream_kernel(W4GemmArgs g, uint64_t per_group) {
   constexpr int F = FOLD > 4 ? 4 : FOLD, NS = 4 / F, kSlot = 16384;  // NS: scales of a block of 128
-  using Lds = ScaleLds<FMT, SIZE, NT>;
+  constexpr int kUnit = FOLD < 4 ? 64 : 32;
+  using Lds = ScaleLds<FMT, SIZE, NT, kUnit>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][kSlot];
   __shared__ __attribute__((aligned(16))) uint8_t scale_lds[4][Lds::kBytes];
   const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, q4 = lane >> 4;
@@ -649,11 +679,20 @@ __global__ __launch_bounds__(256, STREAM_OCC) void w4_stream_kernel(W4GemmArgs g
     Sums<FMT, 1, NT> sums;
     sums.clear();
     u32x4 q[4][NT], xv[1];
-    ScaleLoad<FMT, SIZE, NT> sc;
-    const auto codes = [&](int b, u32x4 (&v)[NT]) {
+    ScaleLoad<FMT, SIZE, NT, kUnit> sc;
+    constexpr int kLast = FOLD > 4 ? 1 : 4 / NS;
+    Items<kLast * NS, SIZE> bs[NT];
+    Items<kLast * NS, 1> bz[NT];
+    const bool quads = (ng & 3) == 0;
+    // two blocks, 128 bytes of each row, together: asked for one at a time, a cache line's second half came so late that it had to be
+    // fetched again
+    const auto codes = [&](int b, u32x4 (&v)[NT], u32x4 (&w)[NT]) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        v[t] = *(const MOE_GLOBAL u32x4*)(scalar(c.q[t] + (long long)b * 64) + vector(c.q_off[t]));
+      for (int t = 0; t < NT; ++t) {
+        const gptr p = scalar(c.q[t] + (long long)b * 64) + vector(c.q_off[t]);
+        v[t] = *(const MOE_GLOBAL u32x4*)p;
+        w[t] = *(const MOE_GLOBAL u32x4*)(p + 64);
+      }
     };
     const auto group_of = [&](int b) { return FOLD > 4 ? (int)((uint32_t)b * per_group >> 32) : b * NS; };
     // block i of the 512 of K at sb
@@ -663,32 +702,34 @@ __global__ __launch_bounds__(256, STREAM_OCC) void w4_stream_kernel(W4GemmArgs g
         return *reinterpret_cast<const u32x4*>(base + xoff[j & 3] + ((i + j / 4) & 3) * 256);
       };
       if (i == 0) xv[0] = x(0, 0);
-      Items<NS, SIZE> s[NT];
-      Items<NS, 1> z[NT];
-      const int at = group_of(sb * 4 + i) & 63;
+      // scales and zero points of as many blocks as four groups make, or of one block where they are larger
+      if (i % kLast == 0) {
+        const int at = group_of(sb * 4 + i) & (kUnit - 1);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        s[t].load_lds(sl.scales(t) + at * SIZE);
-        if constexpr (FMT == kInt4) z[t].load_lds(sl.zeros(t) + at);
+        for (int t = 0; t < NT; ++t) {
+          bs[t].load_lds(sl.scales(t) + at * SIZE);
+          if constexpr (FMT == kInt4) bz[t].load_lds(sl.zeros(t) + at);
+        }
       }
       multiply<XT, FMT, true, F, 1, NT>(
-          q[i], xv, x, [&](int t, int f) { return scale_value<SIZE>(s[t].get(f), g.scale_dtype); },
-          [&](int t, int f) { return g.zeros != nullptr ? (float)z[t].get(f) : 8.f; }, sums);
+          q[i], xv, x, [&](int t, int f) { return scale_value<SIZE>(bs[t].get(i % kLast * NS + f), g.scale_dtype); },
+          [&](int t, int f) { return g.zeros != nullptr ? (float)bz[t].get(i % kLast * NS + f) : 8.f; }, sums);
     };
     // the scales where the 512 of K at sb are the first that need them, and the next ones' loads
     int unit = 0;
     const auto turn_scales = [&](int sb) {
-      if (group_of(sb * 4) >> 6 == unit) {
-        sl.put(sc);
+      if (group_of(sb * 4) / kUnit == unit) {
+        if (quads) sl.put(sc);
+        else sl.copy(g, c, unit * kUnit);
         ++unit;
-        if (unit * 64 < ng) sc.load(g, c, unit);
+        if (quads && unit * kUnit < ng) sc.load(g, c, unit * kUnit);
       }
     };
     fetch(0);
-    sc.load(g, c, 0);
+    if (quads) sc.load(g, c, 0);
     if (nfull > 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) codes(i, q[i]);
+      codes(0, q[0], q[1]);
+      codes(2, q[2], q[3]);
     }
     put(0);
     for (int slot = 0, sb = 0; slot < nslots; ++slot) {
@@ -701,7 +742,7 @@ __global__ __launch_bounds__(256, STREAM_OCC) void w4_stream_kernel(W4GemmArgs g
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           block(slot, sb, i);
-          codes(next * 4 + i, q[i]);
+          if (i & 1) codes(next * 4 + i - 1, q[i - 1], q[i]);
         }
       }
       if (slot == nslots - 1 && nfull < nsb) {  // less than 512 at the end
@@ -725,24 +766,25 @@ __global__ __launch_bounds__(256, STREAM_OCC) void w4_stream_kernel(W4GemmArgs g
   }
 }
 
-// Up to 64 rows at a time: a workgroup of four waves, 32 weight rows each.  The rows' values are brought to LDS by all four, 256
-// of K at a time into one of two slots; the codes come two blocks of 128 ahead.
-template <typename XT, int FMT, int SIZE, int FOLD, int RT>
-__device__ __forceinline__ void tile_rows(const W4GemmArgs& g, uint64_t per_group, uint8_t (*lds)[64 * 512],
+// Up to kTileRows rows at a time: a workgroup of four waves, 32 weight rows each.  The rows' values are brought to LDS by all four, 128 of
+// K at a time into one of two slots; the codes come a block of 128 ahead of that.
+constexpr int kTileRows = 64;
+template <typename XT, int FMT, int SIZE, int FOLD, int RT, typename Lds>
+__device__ __forceinline__ void tile_rows(const W4GemmArgs& g, uint64_t per_group, uint8_t (*lds)[kTileRows * 256], const Lds& sl,
                                           const Columns<SIZE, 2>& c, bool mine, int m0, int m_end) {
+  constexpr int F = FOLD > 4 ? 4 : FOLD, NS = 4 / F, kUnit = Lds::kPart * 4;
   const int lane = threadIdx.x & 63, r16 = lane & 15, q4 = lane >> 4, tid = threadIdx.x;
-  const int nfull = g.K / 128, nblk = (g.K + 127) / 128;
-  // thread: 16-byte chunk tid % 16 of a block of rows tid / 16 + 16 m; the low four bits of a chunk's number are turned by the
-  // row's, so that 16 rows' equal chunks lie in different banks
+  const int nfull = g.K / 128, nblk = (g.K + 127) / 128, ng = g.K / g.G;
+  // thread: 16-byte chunk tid % 16 of a block of rows tid / 16 + 16 m; a chunk's number is turned by the row's, so that 16 rows' equal
+  // chunks lie in different banks
   const int srow = tid >> 4, chunk = tid & 15;
   const XT* src[RT];
 #pragma unroll
   for (int m = 0; m < RT; ++m)
     src[m] = static_cast<const XT*>(g.A) + (long long)min(m0 + m * 16 + srow, m_end - 1) * g.a_stride + chunk * 8;
   u32x4 stage[RT];
-  // the rows' values of block b, zero past K
-  const auto fetch = [&](int b) {
-    const bool in = FOLD == 4 || b * 128 + chunk * 8 < g.K;
+  const auto fetch = [&](int b) {  // the rows' values of block b, zero past K
+    const bool in = FOLD >= 4 || b * 128 + chunk * 8 < g.K;
 #pragma unroll
     for (int m = 0; m < RT; ++m) {
       stage[m] = load_row16(vector(src[m] + (in ? b * 128 : 0)));
@@ -750,55 +792,78 @@ __device__ __forceinline__ void tile_rows(const W4GemmArgs& g, uint64_t per_grou
     }
   };
   const auto put = [&](int b) {
-    uint8_t* at = lds[(b >> 1) & 1] + (b & 1) * 256 + srow * 512 + ((chunk ^ srow) & 15) * 16;
+    uint8_t* at = lds[b & 1] + srow * 256 + ((chunk ^ srow) & 15) * 16;
 #pragma unroll
-    for (int m = 0; m < RT; ++m) *reinterpret_cast<u32x4*>(at + m * 16 * 512) = stage[m];
+    for (int m = 0; m < RT; ++m) *reinterpret_cast<u32x4*>(at + m * 16 * 256) = turn<FMT>(stage[m]);
   };
   int xoff[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) xoff[j] = r16 * 512 + (((FOLD == 4 ? q4 * 4 + j : j * 4 + q4) ^ r16) * 16);
+  for (int j = 0; j < 4; ++j) xoff[j] = r16 * 256 + (((F == 4 ? q4 * 4 + j : j * 4 + q4) ^ r16) * 16);
   Sums<FMT, RT, 2> sums;
   sums.clear();
-  const auto step = [&](int b, Codes<FMT, SIZE, FOLD, 2>& codes) {
-    const uint8_t* at = lds[(b >> 1) & 1] + (b & 1) * 256;
-    const auto x = [&](int m, int j) { return *reinterpret_cast<const u32x4*>(at + m * 16 * 512 + xoff[j & 3]); };
+  const auto codes = [&](int b, u32x4 (&q)[2]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) q[t] = *(const MOE_GLOBAL u32x4*)(scalar(c.q[t] + (long long)b * 64) + vector(c.q_off[t]));
+  };
+  const auto group_of = [&](int b) { return FOLD > 4 ? (int)((uint32_t)b * per_group >> 32) : b * NS; };
+  int base = -kUnit;  // first group in LDS
+  const auto step = [&](int b, u32x4 (&q)[2]) {
+    if (group_of(b) >= base + kUnit) {
+      base += kUnit;
+      if ((ng & 3) == 0) {
+        ScaleLoad<FMT, SIZE, 2, kUnit> sc;
+        sc.load(g, c, base);
+        sl.put(sc);
+      } else {
+        sl.copy(g, c, base);
+      }
+    }
+    Items<NS, SIZE> s[2];
+    Items<NS, 1> z[2];
+    const int at = group_of(b) - base;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      s[t].load_lds(sl.scales(t) + at * SIZE);
+      if constexpr (FMT == kInt4) z[t].load_lds(sl.zeros(t) + at);
+    }
+    const uint8_t* p = lds[b & 1];
+    const auto x = [&](int m, int j) { return *reinterpret_cast<const u32x4*>(p + m * 16 * 256 + xoff[j & 3]); };
     u32x4 v[RT];
 #pragma unroll
     for (int m = 0; m < RT; ++m) v[m] = x(m, 0);
-    codes.template multiply_into<XT>(g, v, x, sums);
+    multiply<XT, FMT, true, F, RT, 2>(
+        q, v, x, [&](int t, int f) { return scale_value<SIZE>(s[t].get(f), g.scale_dtype); },
+        [&](int t, int f) { return g.zeros != nullptr ? (float)z[t].get(f) : 8.f; }, sums);
   };
-  // Blocks go in pairs, a slot each; a last odd or partial one is read with its conditions.  No load is under a condition
-  // before that: past the last pair the same one is read again
-  const int npairs = nfull / 2;
-  Codes<FMT, SIZE, FOLD, 2> c0, c1;
+  // no load of codes or rows is under a condition: past the last whole block the same one is read again
+  u32x4 q0[2], q1[2];
   fetch(0);
+  if (nfull > 0) {
+    codes(0, q0);
+    codes(min(1, nfull - 1), q1);
+  }
   put(0);
-  if (nblk > 1) {
-    fetch(1);
-    put(1);
-  }
-  if (npairs > 0) {
-    c0.template load<true>(g, c, 0, per_group);
-    c1.template load<true>(g, c, 1, per_group);
-  }
-  for (int p = 0; p < npairs; ++p) {
+  const auto turn_block = [&](int b, u32x4 (&q)[2]) {
     __syncthreads();  // this slot is written, and the other one's readers are done
-    const int to = min(p + 1, npairs - 1) * 2, xto = min(2 * p + 2, nblk - 1);
-    fetch(xto);
-    step(2 * p, c0);
-    c0.template load<true>(g, c, to, per_group);
-    put(2 * p + 2);
-    fetch(min(xto + 1, nblk - 1));
-    step(2 * p + 1, c1);
-    c1.template load<true>(g, c, to + 1, per_group);
-    put(2 * p + 3);
+    fetch(min(b + 1, nblk - 1));
+    step(b, q);
+    codes(min(b + 2, nfull - 1), q);
+    put(b + 1);
+  };
+  int b = 0;
+  for (; b + 1 < nfull; b += 2) {
+    turn_block(b, q0);
+    turn_block(b + 1, q1);
   }
-  if (npairs * 2 < nblk) {
+  if (b < nfull) turn_block(b, q0);
+  if (FOLD < 4 && nfull < nblk) {  // the last, partial block
     __syncthreads();
-    for (int b = npairs * 2; b < nblk; ++b) {
-      c0.template load<false>(g, c, b, per_group);
-      step(b, c0);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      q0[t] = u32x4{0, 0, 0, 0};
+      if (nfull * 128 + q4 * 32 < g.K) q0[t] = *reinterpret_cast<const u32x4*>(c.q[t] + nfull * 64LL + c.q_off[t]);
     }
+    step(nfull, q0);
   }
   sums.finish();
   if (mine) finish<XT, FMT>(g, sums.acc, c, m0, m_end);
@@ -807,18 +872,22 @@ __device__ __forceinline__ void tile_rows(const W4GemmArgs& g, uint64_t per_grou
 
 template <typename XT, int FMT, int SIZE, int FOLD>
 __global__ __launch_bounds__(256, 2) void w4_tile_kernel(W4GemmArgs g, uint64_t per_group) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][64 * 512];
+  using Lds = ScaleLds<FMT, SIZE, 2, 32>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][kTileRows * 256];
+  __shared__ __attribute__((aligned(16))) uint8_t scale_lds[4][Lds::kBytes];
   const int e = blockIdx.y, cols = g.act >= 0 ? 16 : 32;
   const int2 rr = expert_rows(g.offsets, e, g.rows);
   const long long column = (long long)(blockIdx.x * 4 + wave_id()) * cols;
   const bool mine = column < g.N;  // a wave without columns helps with the rows
   Columns<SIZE, 2> c;
   c.init(g, e, mine ? (int)column : 0);
-  for (long long m = rr.x + (long long)blockIdx.z * 64; m < rr.y; m += (long long)gridDim.z * 64) {
-    const int m0 = (int)m, rows = rr.y - m0;
-    if (rows <= 16) tile_rows<XT, FMT, SIZE, FOLD, 1>(g, per_group, lds, c, mine, m0, rr.y);
-    else if (rows <= 32) tile_rows<XT, FMT, SIZE, FOLD, 2>(g, per_group, lds, c, mine, m0, rr.y);
-    else tile_rows<XT, FMT, SIZE, FOLD, 4>(g, per_group, lds, c, mine, m0, rr.y);
+  const Lds sl{scale_lds[wave_id()] + (threadIdx.x & 15) * Lds::kS};
+  for (long long m = rr.x + (long long)blockIdx.z * kTileRows; m < rr.y; m += (long long)gridDim.z * kTileRows) {
+    const int m0 = (int)m, rows = min(kTileRows, rr.y - m0), end = m0 + rows;
+    if (rows <= 16) tile_rows<XT, FMT, SIZE, FOLD, 1>(g, per_group, lds, sl, c, mine, m0, end);
+    else if (rows <= 32) tile_rows<XT, FMT, SIZE, FOLD, 2>(g, per_group, lds, sl, c, mine, m0, end);
+    else if (rows <= 48) tile_rows<XT, FMT, SIZE, FOLD, 3>(g, per_group, lds, sl, c, mine, m0, end);
+    else tile_rows<XT, FMT, SIZE, FOLD, 4>(g, per_group, lds, sl, c, mine, m0, end);
   }
 }
 
@@ -826,19 +895,26 @@ template <typename XT, int FMT, int SIZE, int FOLD>
 hipError_t launch(const W4GemmArgs& g, hipStream_t s) {
   const int bpg = g.G / 128;
   const uint64_t per_group = bpg > 0 ? (0x100000000ULL + bpg - 1) / bpg : 0;
+  // row tiles beyond those of evenly filled experts are taken in turn
   const auto go = [&](auto kern, int columns, int threads, int rows) {
-    const int z = (g.rows + rows - 1) / rows, most = g.groups == 1 ? 1024 : 4;
-    kern<<<dim3((g.N + columns - 1) / columns, g.groups, z < most ? z : most), threads, 0, s>>>(g, per_group);
+    const long long z = (g.rows + (long long)rows * g.groups - 1) / ((long long)rows * g.groups);
+    kern<<<dim3((g.N + columns - 1) / columns, g.groups, z < 1024 ? z : 1024), threads, 0, s>>>(g, per_group);
     return hipGetLastError();
   };
   const bool act = g.act >= 0;
-  constexpr int F = FOLD > 4 ? 4 : FOLD;
-  if (g.rows > 16 && g.rows > 8LL * g.groups) return go(w4_tile_kernel<XT, FMT, SIZE, F>, act ? 64 : 128, 256, 64);
-  // tiles of 32 weight rows; while they fill the GPU's waves, one wave for each
-  const long long tiles = (long long)g.groups * ((g.N + 15) / 16) * (act ? 2 : 1) / 2;
-  if (tiles >= 256) return go(w4_stream_kernel<XT, FMT, SIZE, FOLD, STREAM_NT>, act ? 32 * STREAM_NT : 64 * STREAM_NT, 256, 16);
-  if (act || tiles >= 512) return go(w4_few_kernel<XT, FMT, SIZE, F, 2, 8>, act ? 16 : 32, 512, 16);
-  return go(w4_few_kernel<XT, FMT, SIZE, F, 1, 16>, 16, 1024, 16);
+  // Up to 16 rows an expert the weights are read once either way.  Above, the tile kernel reads them once for 64 rows, but its workgroups are
+  // long: with less than one for each CU the few-rows kernel, a round for every 16 rows, is faster up to 64 rows an expert (64 rows through
+  // 8192 x 8192: 41 us and 64; 128 rows: 79 and 64; 24 rows in each of 32 experts of 4096 x 4096: 143 and 110).
+  const long long avg = (g.rows + g.groups - 1) / g.groups, wide = act ? 64 : 128;
+  const long long workgroups = g.groups * ((g.N + wide - 1) / wide);
+  if (avg > 64 || (avg > 16 && workgroups >= 256)) return go(w4_tile_kernel<XT, FMT, SIZE, FOLD>, (int)wide, 256, kTileRows);
+  // Each wave of the stream kernel reads its own rows' whole length, the few-rows kernel's waves share a row: many rows keep the card
+  // busy with the first (32 experts of 4096 x 7168, 4 rows each: 105 us and 118), fewer with the second (16 experts of 7168 x 2048: 66
+  // and 60; 4096 x 7168 alone: 8.9 and 6.1), which takes 32 weight rows a workgroup or, where that gives too few, 16
+  const long long weight_rows = (long long)g.groups * g.N * (act ? 2 : 1);
+  if (weight_rows >= 98304) return go(w4_stream_kernel<XT, FMT, SIZE, FOLD, 2>, (int)wide, 256, 16);
+  if (act || weight_rows > 8192) return go(w4_few_kernel<XT, FMT, SIZE, FOLD, 2, 4>, act ? 16 : 32, 256, 16);
+  return go(w4_few_kernel<XT, FMT, SIZE, FOLD, 1, 4>, 16, 256, 16);
 }
 
 template <typename XT, int SIZE>

@@ -181,15 +181,73 @@ def test_whole_numbers_are_exact(sizes, N, kg, form, group, zeros, dtype):
     assert (c[:, N:] == 77).all()
 
 
-def sum_bound(x, w, s, z, form, group, dtype):
-    """How far the float32 sums may be off: bf16 rows multiply 16 + q, and (16 + z) sum x comes off; each of a group's sums
-    takes `group` additions, then a product and an addition of groups for each, then the waves'."""
+LARGE = [  # rows of each expert, N, K in blocks of 128: enough weight rows for long runs of few rows, and for tiles of many
+    ([1], 98500, 3), ([3, 0, 8, 16], 24700, 5), ([1, 1], 49300, 17), ([17, 64, 0, 33, 1, 49, 20, 16], 4100, 5),
+    ([200, 1, 66], 1000, 17), ([40, 0, 0, 500], 8300, 3), ([12] * 5, 1700, 18)]
+
+
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("form,group,zeros", FORMS)
+@pytest.mark.parametrize("sizes,N,blocks", LARGE)
+def test_large_shapes(sizes, N, blocks, form, group, zeros, dtype, act):
+    """Shapes with many weight rows, some of whose columns are checked; whole numbers again, exact before the activation.  Groups of 32 and 64
+    end inside a block of 128."""
+    K = blocks * 128 + (group if group < 128 else 0)
+    if group > 128:
+        K = -(-K // group) * group
+    E, R = len(sizes), sum(sizes)
+    N = N if act is None else (N + 1) // 2
+    n2 = N if act is None else 2 * N
+    g = torch.Generator(device="cuda").manual_seed(N + K)
+    scale = ["bf16", "f16", "f32"][(len(sizes) + blocks) % 3]
+    b = torch.randint(0, 256, (E, n2, K // 2), generator=g, dtype=torch.uint8, device="cuda")
+    shape, z = (E, n2, K // group), None
+    if form == "mxfp4":
+        scale = "ue8m0"
+        s = torch.randint(125, 130, shape, generator=g, dtype=torch.uint8, device="cuda")
+    else:
+        s = torch.exp2(torch.randint(-2, 3, shape, generator=g, device="cuda").float()).to(DT[scale])
+        if zeros:
+            z = torch.randint(0, 16, shape, generator=g, dtype=torch.uint8, device="cuda")
+    x = torch.randint(-2, 3, (R, K), generator=g, device="cuda").to(DT[dtype])
+    c = torch.full((R + 1, N), 77.0, device="cuda")
+    d = B.make_w4_gemm_desc(R, N, K, E, form, group, scale, zeros, dtype, "f32", act)
+    B.moe_w4_gemm(d, x, b, s, z, offsets_of(sizes).cuda(), c[:R])
+    cols = torch.unique(torch.cat([torch.arange(40), torch.arange(N // 2, N // 2 + 70), torch.arange(N - 40, N)]))
+    at = (cols if act is None else torch.cat([cols, N + cols])).cuda()
+    got = c[:R, cols.cuda()].cpu().double()
+    r0 = 0
+    for e, n in enumerate(sizes):
+        q = b[e, at].cpu()
+        q = torch.stack([q & 15, q >> 4], -1).reshape(len(at), K)
+        sc = s[e, at].cpu()
+        if form == "mxfp4":
+            w = torch.from_numpy(E2M1)[q.long()] * torch.exp2(sc.double() - 127).repeat_interleave(group, -1)
+        else:
+            w = (q.double() - (8 if z is None else z[e, at].cpu().double().repeat_interleave(group, -1))) * \
+                sc.double().repeat_interleave(group, -1)
+        y = x[r0:r0 + n].cpu().double() @ w.t()
+        if act is None:
+            assert torch.equal(got[r0:r0 + n], y), e
+        else:
+            # the sums are exact; the activation takes an exponential, an addition, a division and a product, a few roundings each;
+            # where it underflows float32 it is 0
+            want = act_ref(y, act, 0, 0, 0)
+            assert ((got[r0:r0 + n] - want).abs() <= want.abs() * 2.0 ** -20 + 1e-30 * y.chunk(2, -1)[1].abs()).all(), e
+        r0 += n
+    assert (c[R] == 77).all()
+
+
+def sum_bound(x, w, s, z, form, group):
+    """How far the float32 sums may be off: the codes' products and the zero point's are summed apart, |x| (q + z) together at most, each
+    sum of a group takes `group` additions, then come a product and an addition for each group, and the waves'."""
     K = x.shape[-1]
     sd = s.double() if form == "int4" else torch.exp2(s.double() - 127)
     ax = x.abs()
-    if form == "int4" and dtype == "bf16":
+    if form == "int4":
         zz = torch.full(s.shape, 8.0, dtype=torch.float64) if z is None else z.double()
-        inner = ax @ ((16 + 15 + 16 + zz) * sd).repeat_interleave(group, -1).t()
+        inner = ax @ ((15 + zz) * sd).repeat_interleave(group, -1).t()
     else:
         inner = ax @ w.abs().t()
     return inner * (group + 4) * U + (ax @ w.abs().t()) * (K // group + 20) * U
@@ -217,7 +275,7 @@ def test_product(sizes, N, K, form, group, zeros, scale, dtype, out, act):
     for e, n in enumerate(sizes):
         xe = x[r0:r0 + n].double()
         y = xe @ w[e].t()
-        err = sum_bound(xe, w[e], s[e], None if z is None else z[e], form, group, dtype)
+        err = sum_bound(xe, w[e], s[e], None if z is None else z[e], form, group)
         want = act_ref(y, act, clamp, alpha, bias)
         if act is not None:
             # |d act / d gate| <= 1.2 max(1, alpha) |up|, |d act / d up| <= |gate|; and the function's own few roundings
