@@ -774,7 +774,7 @@ __device__ __forceinline__ void tile_rows(const W4GemmArgs& g, uint64_t per_grou
                                           const Columns<SIZE, 2>& c, bool mine, int m0, int m_end) {
   constexpr int F = FOLD > 4 ? 4 : FOLD, NS = 4 / F, kUnit = Lds::kPart * 4;
   const int lane = threadIdx.x & 63, r16 = lane & 15, q4 = lane >> 4, tid = threadIdx.x;
-  const int nfull = g.K / 128, nblk = (g.K + 127) / 128, ng = g.K / g.G;
+  const int nfull = g.K / 128, ng = g.K / g.G;
   // thread: 16-byte chunk tid % 16 of a block of rows tid / 16 + 16 m; a chunk's number is turned by the row's, so that 16 rows' equal
   // chunks lie in different banks
   const int srow = tid >> 4, chunk = tid & 15;
@@ -783,13 +783,9 @@ __device__ __forceinline__ void tile_rows(const W4GemmArgs& g, uint64_t per_grou
   for (int m = 0; m < RT; ++m)
     src[m] = static_cast<const XT*>(g.A) + (long long)min(m0 + m * 16 + srow, m_end - 1) * g.a_stride + chunk * 8;
   u32x4 stage[RT];
-  const auto fetch = [&](int b) {  // the rows' values of block b, zero past K
-    const bool in = FOLD >= 4 || b * 128 + chunk * 8 < g.K;
+  const auto fetch = [&](int b) {  // the rows' values of block b
 #pragma unroll
-    for (int m = 0; m < RT; ++m) {
-      stage[m] = load_row16(vector(src[m] + (in ? b * 128 : 0)));
-      if (!in) stage[m] = u32x4{0, 0, 0, 0};
-    }
+    for (int m = 0; m < RT; ++m) stage[m] = load_row16(vector(src[m] + b * 128));
   };
   const auto put = [&](int b) {
     uint8_t* at = lds[b & 1] + srow * 256 + ((chunk ^ srow) & 15) * 16;
@@ -837,15 +833,15 @@ __device__ __forceinline__ void tile_rows(const W4GemmArgs& g, uint64_t per_grou
   };
   // no load of codes or rows is under a condition: past the last whole block the same one is read again
   u32x4 q0[2], q1[2];
-  fetch(0);
   if (nfull > 0) {
+    fetch(0);
     codes(0, q0);
     codes(min(1, nfull - 1), q1);
+    put(0);
   }
-  put(0);
   const auto turn_block = [&](int b, u32x4 (&q)[2]) {
     __syncthreads();  // this slot is written, and the other one's readers are done
-    fetch(min(b + 1, nblk - 1));
+    fetch(min(b + 1, nfull - 1));
     step(b, q);
     codes(min(b + 2, nfull - 1), q);
     put(b + 1);
@@ -856,7 +852,15 @@ __device__ __forceinline__ void tile_rows(const W4GemmArgs& g, uint64_t per_grou
     turn_block(b + 1, q1);
   }
   if (b < nfull) turn_block(b, q0);
-  if (FOLD < 4 && nfull < nblk) {  // the last, partial block
+  if (FOLD < 4 && nfull * 128 < g.K) {  // the last, partial block, zeros past K
+    __syncthreads();
+    const bool in = nfull * 128 + chunk * 8 < g.K;
+#pragma unroll
+    for (int m = 0; m < RT; ++m) {
+      stage[m] = u32x4{0, 0, 0, 0};
+      if (in) stage[m] = load_row16(vector(src[m] + nfull * 128));
+    }
+    put(nfull);
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -882,8 +886,11 @@ __global__ __launch_bounds__(256, 2) void w4_tile_kernel(W4GemmArgs g, uint64_t 
   Columns<SIZE, 2> c;
   c.init(g, e, mine ? (int)column : 0);
   const Lds sl{scale_lds[wave_id()] + (threadIdx.x & 15) * Lds::kS};
-  for (long long m = rr.x + (long long)blockIdx.z * kTileRows; m < rr.y; m += (long long)gridDim.z * kTileRows) {
-    const int m0 = (int)m, rows = min(kTileRows, rr.y - m0), end = m0 + rows;
+  // an expert's rows in as few parts as there can be, of equal numbers of tiles of 16
+  const int all = (int)(((long long)rr.y - rr.x + 15) / 16), parts = (all + kTileRows / 16 - 1) / (kTileRows / 16);
+  const int most = 16 * ((all + max(parts, 1) - 1) / max(parts, 1));
+  for (long long m = rr.x + (long long)blockIdx.z * most; m < rr.y; m += (long long)gridDim.z * most) {
+    const int m0 = (int)m, rows = min(most, rr.y - m0), end = m0 + rows;
     if (rows <= 16) tile_rows<XT, FMT, SIZE, FOLD, 1>(g, per_group, lds, sl, c, mine, m0, end);
     else if (rows <= 32) tile_rows<XT, FMT, SIZE, FOLD, 2>(g, per_group, lds, sl, c, mine, m0, end);
     else if (rows <= 48) tile_rows<XT, FMT, SIZE, FOLD, 3>(g, per_group, lds, sl, c, mine, m0, end);
@@ -895,9 +902,10 @@ template <typename XT, int FMT, int SIZE, int FOLD>
 hipError_t launch(const W4GemmArgs& g, hipStream_t s) {
   const int bpg = g.G / 128;
   const uint64_t per_group = bpg > 0 ? (0x100000000ULL + bpg - 1) / bpg : 0;
-  // row tiles beyond those of evenly filled experts are taken in turn
+  // Rows' parts beyond those of evenly filled experts are taken in turn; where parts are large, by one more workgroup (32 experts, 62.5
+  // rows on average, 42% of them above 64: 207 -> 194 us)
   const auto go = [&](auto kern, int columns, int threads, int rows) {
-    const long long z = (g.rows + (long long)rows * g.groups - 1) / ((long long)rows * g.groups);
+    const long long z = (g.rows + (long long)rows * g.groups - 1) / ((long long)rows * g.groups) + (rows > 16 && g.groups > 1);
     kern<<<dim3((g.N + columns - 1) / columns, g.groups, z < 1024 ? z : 1024), threads, 0, s>>>(g, per_group);
     return hipGetLastError();
   };
