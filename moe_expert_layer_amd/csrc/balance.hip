@@ -179,7 +179,7 @@ struct Parts {
   int32_t* done;  // [S]
 };
 
-constexpr int kSlice = 32;  // columns that a workgroup of the second kernel adds up
+constexpr int kSlice = 8;  // columns that a workgroup of the second kernel adds up, or 32
 
 // A piece's tokens [a, b): probability sums, counts, sum of squared logarithms and tokens, in LDS (psum, hist) and in
 // every thread (z, n).  A workgroup of NW waves, all of them here.
@@ -195,6 +195,10 @@ struct Piece {
                                       const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask, int a, int e,
                                       bool want_z, float& z, int& n) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane & (LPT - 1);
+    int t = a + wave * GPW + lane / LPT;
+    typename Quad<T>::raw next[R] = {};
+    bool counted = t < e && (mask == nullptr || mask[t]);
+    if (t < e) cols.load(logits + (long long)t * b.logit_stride, b.E, next);
     for (int i = tid; i < b.E; i += NW * 64) hist[i] = 0;
     __syncthreads();
     for (long long i = (long long)a * b.k + tid; i < (long long)e * b.k; i += NW * 64) {
@@ -207,10 +211,6 @@ struct Piece {
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[r][i] = 0.f;
-    int t = a + wave * GPW + lane / LPT;
-    typename Quad<T>::raw next[R] = {};
-    bool counted = t < e && (mask == nullptr || mask[t]);
-    if (t < e) cols.load(logits + (long long)t * b.logit_stride, b.E, next);
     while (__any(t < e)) {
       float x[R][4], p[R][4], top, sum;
 #pragma unroll
@@ -332,24 +332,26 @@ __device__ __forceinline__ float balance_of(double cp, int E, int k, double n) {
   return n == 0.0 ? 0.f : (float)(cp * (double)E / ((double)k * n * n));
 }
 
-// workgroup (slice, s): sums the pieces of kSlice columns of sequence s, in float64; the last workgroup of a sequence to
+// workgroup (slice, s): sums the pieces of SL columns of sequence s, in float64; the last workgroup of a sequence to
 // end adds up the slices' parts of its loss, in their order
+template <int SL>
 __global__ __launch_bounds__(512) void balance_join_kernel(BalanceShape b, const int32_t* __restrict__ offsets, int C,
                                                            Parts parts, int32_t* __restrict__ counts,
                                                            int32_t* __restrict__ tokens, float* __restrict__ psum,
                                                            float* __restrict__ balance, float* __restrict__ zloss) {
-  constexpr int NR = 512 / kSlice;
-  __shared__ double sums[NR][kSlice + 1];
-  __shared__ int32_t cnts[NR][kSlice];
+  constexpr int NR = 512 / SL;
+  __shared__ double sums[NR][SL + 1];
+  __shared__ int32_t cnts[NR][SL];
   __shared__ double scratch[8];
   __shared__ int last;
-  const int tid = threadIdx.x, col = tid % kSlice, rl = tid / kSlice, s = blockIdx.y;
-  const int e = blockIdx.x * kSlice + col;
+  const int tid = threadIdx.x, col = tid % SL, rl = tid / SL, s = blockIdx.y;
+  const int e = blockIdx.x * SL + col;
   const int2 range = sequence(offsets, s, b.T);
   const int c0 = range.x / C, c1 = range.y > range.x ? (range.y - 1) / C + 1 : c0;
   double p = 0.0;
   int n = 0;
   if (e < b.E)
+#pragma unroll 4
     for (int c = c0 + rl; c < c1; c += NR) {
       const long long row = c + s;
       p += (double)parts.psum[row * b.E + e];
@@ -359,7 +361,7 @@ __global__ __launch_bounds__(512) void balance_join_kernel(BalanceShape b, const
   cnts[rl][col] = n;
   __syncthreads();
   double part = 0.0;
-  if (tid < kSlice) {
+  if (tid < SL) {
     for (int r = 1; r < NR; ++r) {
       p += sums[r][col];
       n += cnts[r][col];
@@ -385,9 +387,10 @@ __global__ __launch_bounds__(512) void balance_join_kernel(BalanceShape b, const
   }
   z = block_sum(z, scratch, 8);
   nt = block_sum(nt, scratch, 8);
+  double cp = 0.0;
+  for (unsigned i = tid; i < gridDim.x; i += 512) cp += __hip_atomic_load(slot + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  cp = block_sum(cp, scratch, 8);
   if (tid == 0) {
-    double cp = 0.0;
-    for (unsigned i = 0; i < gridDim.x; ++i) cp += __hip_atomic_load(slot + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     tokens[s] = (int)nt;
     balance[s] = balance_of(cp, b.E, b.k, nt);
     if (zloss != nullptr) zloss[s] = nt == 0.0 ? 0.f : (float)(z / nt);
@@ -592,9 +595,14 @@ hipError_t forward(const BalanceShape& b, const void* logits, const int32_t* ids
     balance_parts_kernel<T, LPT, R, kWaves><<<chunks_of(b.T), kWaves * 64, 0, s>>>(b, l, ids, mask, offsets, C,
                                                                                   z != nullptr, parts);
     if (const hipError_t e = hipGetLastError()) return e;
-    balance_join_kernel<<<dim3((b.E + kSlice - 1) / kSlice, b.S), 512, 0, s>>>(b, offsets, C, parts, counts, tokens, psum,
-                                                                             balance, z);
-    return hipGetLastError();
+    // Pieces in the hundreds for a sequence are read by more lanes a column (65536 tokens of 256 experts in one: 8 columns a workgroup 22.8 us
+    // for the two kernels, 32 columns 31); of a few pieces it takes longer to join the slices (16385 tokens of 129 experts in 24: 22.5 us and 16.6)
+    const auto join = [&](auto slice) {
+      constexpr int SL = decltype(slice)::value;
+      balance_join_kernel<SL><<<dim3((b.E + SL - 1) / SL, b.S), 512, 0, s>>>(b, offsets, C, parts, counts, tokens, psum, balance, z);
+      return hipGetLastError();
+    };
+    return chunks_of(b.T) >= 64 * b.S ? join(Int<kSlice>()) : join(Int<32>());
   });
 }
 
