@@ -484,7 +484,7 @@ moe_status moe_mxfp4_gemm(const moe_mxfp4_gemm_desc* desc, const uint8_t* a, con
  *     adds 0 to z and has no gradient, but its ids are counted.  NaN (and, with softmax, +inf) makes
  *     its token's probabilities and what they enter NaN.
  *   - Probabilities are float32; sums over tokens run in a fixed order (no atomics in them), partial
- *     sums in float32 over at most a few hundred tokens of one lane, the rest in float64; the counts' integer sums
+ *     sums in float32 over at most 1024 tokens of one lane and its workgroup's others, the rest in float64; the counts' integer sums
  *     do not depend on the order.  The same from run to run.
  *   - Pointers are aligned to their element; add may be dlogits itself, otherwise outputs must not
  *     overlap inputs or each other.  Stream, validation and error rules are those at the top of this file;

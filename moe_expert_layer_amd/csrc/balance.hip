@@ -14,6 +14,9 @@
 // columns a chunk row) a token's maximum and sum are four DPP steps each, for four tokens of a wave at once; a whole wave on a
 // token would take six steps for one.  Sums over tokens stay in the lanes' registers, over all tokens that a lane sees
 // of a piece (the tokens of one workgroup's chunk in one sequence), then over a wave's groups, then over waves.
+//
+// 65536 tokens of 256 float32 logits: forward 15.6 us and 7.2 to join the pieces (14 us at a copy's rate), gradient with another one added to
+// it 40 to 50 us (41); 128 tokens of 32: 3.5 us, 6 with the launch.
 #include <hip/hip_runtime.h>
 #include <cstddef>
 #include <cstdint>
@@ -529,10 +532,11 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceShape b, c
 constexpr int kWaves = 8;     // waves of the forward kernels
 constexpr int kSmall = 1024;  // at most this many tokens: one workgroup a sequence
 
-// tokens of a workgroup's chunk, at most 512 chunks
+// Tokens of a workgroup's chunk: for 512 chunks, two workgroups a CU, but no fewer than a workgroup takes at a time, and no more than leave 1024
+// to the sums of one lane
 int chunk_of(int T) {
   const long long c = ((long long)T + 511) / 512;
-  return (int)(c < 32 ? 32 : c);
+  return (int)(c < 32 ? 32 : c > 8192 ? 8192 : c);
 }
 int chunks_of(int T) { return (int)(((long long)T + chunk_of(T) - 1) / chunk_of(T)); }
 

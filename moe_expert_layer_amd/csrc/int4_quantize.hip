@@ -9,7 +9,8 @@
 //
 // Both directions are bound by HBM.  A lane takes 8 values (one or two 16-byte loads) and leaves 4 bytes of codes; 4, 8 or
 // 16 lanes hold a group of 32, 64 or 128.  Larger groups are walked 128 values at a time by 16 lanes, twice, the second
-// time from the caches.
+// time from the caches.  16384 x 7168 float32 values with groups of 128 and zero points, and
+// back to bf16: 182 us for the two, 156 at a copy's rate (from the caches, 1027 x 2080 bf16 values take 4.8 + 3.9 us).
 #include <hip/hip_runtime.h>
 #include <cstdint>
 

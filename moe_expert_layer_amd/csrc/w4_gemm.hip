@@ -13,6 +13,13 @@
 // With groups of 128 or more, the four quarters' codes are of one group, and step j multiplies dword j of
 // each; with groups of 32 or 64 the dwords are transposed between the quarters first, so that step j has the
 // codes of quarter j, a run of 32.
+//
+// Three kernels: few rows with K split over waves, few rows by many weight rows, and tiles of up to 64 rows (launch has the rule).  With few
+// rows HBM is the bound: 128 rows in 32 experts of 4096 x 7168 take 97 us with groups of 128 and zero points (5.1 TB/s; a copy runs at 4.9), MXFP4
+// weights of 7168 x 2048 61 us (4.2 TB/s: four scales a block of 128 and their sums); one row through 4096 x 7168 7 us, of which a
+// launch is 4.  Tiles are bound by instructions: 2000 rows through 32 experts of 4096 x 4096 with groups of 64 take 174 us, 65 at a
+// copy's rate; of a SIMD's cycles the matrix instructions take 24% and the vector ones 45% (the scaled additions two fifths of
+// those), and two waves a SIMD, all that the registers allow, leave much of the rest empty.
 #include <hip/hip_runtime.h>
 #include <cstdint>
 
@@ -53,19 +60,14 @@ __device__ __forceinline__ uint32_t from_e2m1(uint32_t v) {
   else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, 1.f, B));
 }
 
-// eight codes as 16-bit floats, in their order; INT4 with TURNED: even ones, then odd ones, which saves two permutations where the
-// rows' values have been put in that order once for many weights (turn)
-template <typename XT, int FMT, bool TURNED>
+// Eight codes as 16-bit floats; INT4: even ones, then odd ones, as the nibbles come, the rows' values being put in that order once for many
+// weights (turn)
+template <typename XT, int FMT>
 __device__ __forceinline__ u32x4 widen(uint32_t q) {
-  if constexpr (FMT == kMxfp4) {
+  if constexpr (FMT == kMxfp4)
     return u32x4{from_e2m1<XT, 0>(q), from_e2m1<XT, 1>(q), from_e2m1<XT, 2>(q), from_e2m1<XT, 3>(q)};
-  } else {
-    const uint32_t even = q & 0x0f0f0f0fu, odd = (q >> 4) & 0x0f0f0f0fu;
-    if constexpr (TURNED)
-      return u32x4{from_e4m3<XT, false>(even), from_e4m3<XT, true>(even), from_e4m3<XT, false>(odd), from_e4m3<XT, true>(odd)};
-    const uint32_t a = __builtin_amdgcn_perm(odd, even, 0x05010400u), b = __builtin_amdgcn_perm(odd, even, 0x07030602u);
-    return u32x4{from_e4m3<XT, false>(a), from_e4m3<XT, true>(a), from_e4m3<XT, false>(b), from_e4m3<XT, true>(b)};
-  }
+  const uint32_t even = q & 0x0f0f0f0fu, odd = (q >> 4) & 0x0f0f0f0fu;
+  return u32x4{from_e4m3<XT, false>(even), from_e4m3<XT, true>(even), from_e4m3<XT, false>(odd), from_e4m3<XT, true>(odd)};
 }
 template <int FMT>
 __device__ __forceinline__ u32x4 turn(u32x4 x) {
@@ -296,7 +298,7 @@ struct Sums {
 
 // The products of 128 of K.  q: codes; x(m, j): rows 16 m + lane % 16, the eight values of step j of this lane's quarter (asked for
 // a step ahead; v has those of step 0, and on return those of step 4); scale_of(s, f), zero_of(s, f): of tile s and fold f
-template <typename XT, int FMT, bool TURNED, int FOLD, int RT, int NT, typename X, typename S, typename Z>
+template <typename XT, int FMT, int FOLD, int RT, int NT, typename X, typename S, typename Z>
 __device__ __forceinline__ void multiply(u32x4 (&q)[NT], u32x4 (&v)[RT], X x, S scale_of, Z zero_of, Sums<FMT, RT, NT>& sums) {
   if constexpr (FOLD < 4) {
 #pragma unroll
@@ -321,7 +323,7 @@ __device__ __forceinline__ void multiply(u32x4 (&q)[NT], u32x4 (&v)[RT], X x, S 
       for (int m = 0; m < RT; ++m) ahead[m] = x(m, j + 1);
 #pragma unroll
       for (int s = 0; s < NT; ++s) {
-        w[s] = widen<XT, FMT, TURNED>(q[s][j]);
+        w[s] = widen<XT, FMT>(q[s][j]);
         if constexpr (RT > 1) asm("" : "+v"(w[s]));  // once for all rows' tiles: the compiler widens again for each
       }
 #pragma unroll
@@ -526,7 +528,7 @@ __device__ __forceinline__ void few_rows(const W4GemmArgs& g, uint64_t per_group
     }
     const auto x = [&](int, int j) { return *reinterpret_cast<const u32x4*>(xl + xoff[j & 3]); };
     u32x4 xv[1] = {x(0, 0)};
-    multiply<XT, FMT, true, F, 1, NT>(
+    multiply<XT, FMT, F, 1, NT>(
         k.q, xv, x, [&](int t, int f) { return scale_value<SIZE>(s[t].get(f), g.scale_dtype); },
         [&](int t, int f) { return g.zeros != nullptr ? (float)z[t].get(f) : 8.f; }, sums);
   };
@@ -711,7 +713,7 @@ __global__ __launch_bounds__(256, 2) void w4_stream_kernel(W4GemmArgs g, uint64_
           if constexpr (FMT == kInt4) bz[t].load_lds(sl.zeros(t) + at);
         }
       }
-      multiply<XT, FMT, true, F, 1, NT>(
+      multiply<XT, FMT, F, 1, NT>(
           q[i], xv, x, [&](int t, int f) { return scale_value<SIZE>(bs[t].get(i % kLast * NS + f), g.scale_dtype); },
           [&](int t, int f) { return g.zeros != nullptr ? (float)bz[t].get(i % kLast * NS + f) : 8.f; }, sums);
     };
@@ -827,7 +829,7 @@ __device__ __forceinline__ void tile_rows(const W4GemmArgs& g, uint64_t per_grou
     u32x4 v[RT];
 #pragma unroll
     for (int m = 0; m < RT; ++m) v[m] = x(m, 0);
-    multiply<XT, FMT, true, F, RT, 2>(
+    multiply<XT, FMT, F, RT, 2>(
         q, v, x, [&](int t, int f) { return scale_value<SIZE>(s[t].get(f), g.scale_dtype); },
         [&](int t, int f) { return g.zeros != nullptr ? (float)z[t].get(f) : 8.f; }, sums);
   };

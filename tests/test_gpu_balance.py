@@ -416,3 +416,38 @@ def test_refusals():
         a.update(kw)
         with pytest.raises(B.MoeError):
             B.moe_balance_loss_backward(d, x, c, t, a.pop("dbalance"), a.pop("dlogits"), **a)
+
+
+def test_most_sequences():
+    """As many sequences as there may be, most of them of one token or none, in both directions."""
+    T, E, k, S = 70001, 5, 2, 65536
+    r = np.random.RandomState(3)
+    ends = np.concatenate([[0], np.sort(r.randint(0, T + 1, S - 1)), [T]]).astype(np.int32)
+    case = {"T": T, "S": S, "ends": ends, "mask": None}
+    logits = r.randn(T, E).astype(np.float32)
+    ids = r.randint(0, E, (T, k)).astype(np.int32)
+    db, dz = r.randn(S).astype(np.float32), r.randn(S).astype(np.float32)
+    ref = reference(case, logits.astype(np.float64), ids, k, "softmax", db=db, dz=dz)
+    d = B.make_balance_desc(T, E, k, S, "f32")
+    out = call_forward(d, dev(logits), dev(ids), case, True)
+    check_forward(out, ref)
+    grad = torch.full((T, E), 7.0, device="cuda")
+    B.moe_balance_loss_backward(d, dev(logits), out["counts"], out["tokens"], dev(db), grad, dz=dev(dz), seq_offsets=dev(ends))
+    assert (np.abs(grad.cpu().numpy() - ref["grad"]) <= ref["grad_tol"]).all()
+
+
+def test_millions_of_tokens():
+    """More tokens than 512 chunks of 8192 hold.  |l| < 4, so a probability is (4 * 8 + 88) U off relatively; a lane then adds up to 1024, and 16
+    sums follow."""
+    T, E, k = 4_500_001, 3, 2
+    g = torch.Generator().manual_seed(1)
+    logits = (8 * torch.rand(T, E, generator=g) - 4)
+    ids = torch.randint(-1, E, (T, k), generator=g, dtype=torch.int32)
+    out = call_forward(B.make_balance_desc(T, E, k, 1, "f32"), logits.cuda(), ids.cuda(), {"T": T, "S": 1, "ends": None, "mask": None}, False)
+    p = torch.softmax(logits.double(), 1).sum(0)
+    c = torch.bincount(ids[ids >= 0].long(), minlength=E)
+    assert torch.equal(out["counts"][0].cpu().long(), c) and int(out["tokens"][0]) == T
+    tol = (120 + 1024 + 16 + 1) * U
+    assert ((out["psum"][0].cpu().double() - p).abs() <= p * tol).all()
+    want = float((c * p).sum()) * E / (k * float(T) ** 2)
+    assert abs(float(out["balance"][0]) - want) <= want * (tol + 2 * U)
