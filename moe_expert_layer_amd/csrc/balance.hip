@@ -15,8 +15,8 @@
 // token would take six steps for one.  Sums over tokens stay in the lanes' registers, over all tokens that a lane sees
 // of a piece (the tokens of one workgroup's chunk in one sequence), then over a wave's groups, then over waves.
 //
-// 65536 tokens of 256 float32 logits: forward 15.6 us and 7.2 to join the pieces (14 us at a copy's rate), gradient with another one added to
-// it 40 to 50 us (41); 128 tokens of 32: 3.5 us, 6 with the launch.
+// 65536 tokens of 256 float32 logits: forward 22 us, some 7 of them to join the pieces (14 us at a copy's rate), gradient with another one added
+// to it 39 us (41); 128 tokens of 32: 3.7 us, 6.6 with the launch.
 #include <hip/hip_runtime.h>
 #include <cstddef>
 #include <cstdint>
@@ -435,7 +435,9 @@ __global__ __launch_bounds__(NW * 64) void balance_small_kernel(BalanceShape b, 
   }
 }
 
-// Gradient: groups of LPT lanes take the workgroup's tokens in turn, and keep the counts of their sequence.
+// Gradient: groups of LPT lanes take the workgroup's tokens in turn, and keep the counts of their sequence.  What is read or written once
+// goes past the caches (65536 tokens of 256, 1024 workgroups: 47.4 -> 39.8 us; the logits too: 42.5, and the forward pass has just read them).
+typedef u32x4 at4 __attribute__((aligned(4)));
 template <typename T, int LPT, int R>
 __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceShape b, const T* __restrict__ logits,
                                                                const uint8_t* __restrict__ mask,
@@ -514,11 +516,11 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceShape b, c
         if (((cols.live >> (4 * r)) & 15u) == 15u) {
           if (in != nullptr) {
             float f[4];
-            Quad<float>::get(load16(in + cols.base[r]), f);
+            Quad<float>::get(__builtin_nontemporal_load(reinterpret_cast<const at4*>(in + cols.base[r])), f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[i] += f[i];
           }
-          store16(out + cols.base[r], pack16<float>(d));
+          __builtin_nontemporal_store(pack16<float>(d), reinterpret_cast<at4*>(out + cols.base[r]));
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -532,10 +534,10 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceShape b, c
 constexpr int kWaves = 8;     // waves of the forward kernels
 constexpr int kSmall = 1024;  // at most this many tokens: one workgroup a sequence
 
-// Tokens of a workgroup's chunk: for 512 chunks, two workgroups a CU, but no fewer than a workgroup takes at a time, and no more than leave 1024
-// to the sums of one lane
+// Tokens of a workgroup's chunk: for 256 chunks, one for each CU (256, 512, 1024 of them: 22, 24, 29 us for 65536 tokens of 256, the pieces being
+// joined after), but no fewer than a workgroup takes at a time, and no more than leave 1024 to the sums of one lane
 int chunk_of(int T) {
-  const long long c = ((long long)T + 511) / 512;
+  const long long c = ((long long)T + 255) / 256;
   return (int)(c < 32 ? 32 : c > 8192 ? 8192 : c);
 }
 int chunks_of(int T) { return (int)(((long long)T + chunk_of(T) - 1) / chunk_of(T)); }
@@ -599,7 +601,7 @@ hipError_t forward(const BalanceShape& b, const void* logits, const int32_t* ids
     balance_parts_kernel<T, LPT, R, kWaves><<<chunks_of(b.T), kWaves * 64, 0, s>>>(b, l, ids, mask, offsets, C,
                                                                                   z != nullptr, parts);
     if (const hipError_t e = hipGetLastError()) return e;
-    // Pieces in the hundreds for a sequence are read by more lanes a column (65536 tokens of 256 experts in one: 8 columns a workgroup 22.8 us
+    // Pieces in the hundreds for a sequence are read by more lanes a column (65536 tokens of 256 experts in one: 8 columns a workgroup 22 us
     // for the two kernels, 32 columns 31); of a few pieces it takes longer to join the slices (16385 tokens of 129 experts in 24: 22.5 us and 16.6)
     const auto join = [&](auto slice) {
       constexpr int SL = decltype(slice)::value;
@@ -617,7 +619,9 @@ hipError_t backward(const BalanceShape& b, const void* logits, const uint8_t* ma
   return by_columns(b.E, [&](auto lanes, auto chunks) {
     constexpr int LPT = decltype(lanes)::value, R = decltype(chunks)::value;
     constexpr int TW = 256 / LPT;  // tokens a workgroup has at a time
-    const long long c = ((long long)b.T + 2047) / 2048;
+    // four workgroups a CU, as many as the registers hold at once (65536 tokens of 256: 512, 1024, 1536, 2048, 4096 workgroups 52, 44, 51, 51,
+    // 60 us)
+    const long long c = ((long long)b.T + 1023) / 1024;
     const int C = (int)((c + TW - 1) / TW * TW);
     balance_backward_kernel<T, LPT, R><<<(unsigned)(((long long)b.T + C - 1) / C), 256, 0, s>>>(
         b, static_cast<const T*>(logits), mask, offsets, counts, tokens, dbalance, dz, add, dlogits, C);
