@@ -130,6 +130,17 @@ __device__ __forceinline__ u32x4 load_row16(gptr p) {  // 16 bytes of a row of 1
   return *(const MOE_GLOBAL at2*)p;
 }
 
+// Scales and zero points lie in LDS as bytes that are written in one width and read in another, so both go through types that may
+// alias; and what a lane reads there other lanes of its wave wrote, so a fence stands between.  A wave's LDS instructions run in
+// order: the fence keeps the compiler's order and makes no instruction.
+typedef uint32_t __attribute__((may_alias)) lds_u32;
+typedef uint16_t __attribute__((may_alias)) lds_u16;
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // N (a power of two) consecutive items of SIZE bytes at any alignment of theirs, as they lie; `have`: the first ones only
 template <int N, int SIZE>
 struct Items {
@@ -170,10 +181,10 @@ struct Items {
   }
   __device__ __forceinline__ void load_lds(const uint8_t* p) {
     if constexpr (N * SIZE == 1) w[0] = *p;
-    else if constexpr (N * SIZE == 2) w[0] = *reinterpret_cast<const uint16_t*>(p);
+    else if constexpr (N * SIZE == 2) w[0] = *reinterpret_cast<const lds_u16*>(p);
     else
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+      for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const lds_u32*>(p)[i];
   }
   __device__ __forceinline__ uint32_t get(int i) const {
     if constexpr (SIZE == 4) return w[i];
@@ -450,18 +461,21 @@ struct ScaleLds {
   __device__ __forceinline__ uint8_t* zeros(int t) const { return at + NT * 16 * kS + t * 16 * kZ - (threadIdx.x & 15) * (kS - kZ); }
   __device__ __forceinline__ void put(const ScaleLoad<FMT, SIZE, NT, kUnit>& l) const {
     const int q4 = (threadIdx.x >> 4) & 3;
+    wave_fence();  // the lanes have read what was there
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int i = 0; i < Items<kPart, SIZE>::kWords; ++i) reinterpret_cast<uint32_t*>(scales(t) + q4 * kPart * SIZE)[i] = l.s[t].w[i];
+      for (int i = 0; i < Items<kPart, SIZE>::kWords; ++i) reinterpret_cast<lds_u32*>(scales(t) + q4 * kPart * SIZE)[i] = l.s[t].w[i];
       if constexpr (FMT == kInt4) {
 #pragma unroll
-        for (int i = 0; i < kPart / 4; ++i) reinterpret_cast<uint32_t*>(zeros(t) + q4 * kPart)[i] = l.z[t].w[i];
+        for (int i = 0; i < kPart / 4; ++i) reinterpret_cast<lds_u32*>(zeros(t) + q4 * kPart)[i] = l.z[t].w[i];
       }
     }
+    wave_fence();
   }
   __device__ __forceinline__ void copy(const W4GemmArgs& g, const Columns<SIZE, NT>& c, int base) const {
     const int ng = g.K / g.G, q4 = (threadIdx.x >> 4) & 3;
+    wave_fence();
     for (int i = 0; i < kPart; ++i) {
       const uint32_t at = min(base + q4 * kPart + i, ng - 1);
 #pragma unroll
@@ -469,8 +483,8 @@ struct ScaleLds {
         Items<1, SIZE> v;
         v.load(scalar(c.s[t]) + vector(c.s_off[t] + at * SIZE));
         uint8_t* to = scales(t) + (q4 * kPart + i) * SIZE;
-        if constexpr (SIZE == 4) *reinterpret_cast<uint32_t*>(to) = v.w[0];
-        else if constexpr (SIZE == 2) *reinterpret_cast<uint16_t*>(to) = (uint16_t)v.w[0];
+        if constexpr (SIZE == 4) *reinterpret_cast<lds_u32*>(to) = v.w[0];
+        else if constexpr (SIZE == 2) *reinterpret_cast<lds_u16*>(to) = (uint16_t)v.w[0];
         else *to = (uint8_t)v.w[0];
         if constexpr (FMT == kInt4) {
           Items<1, 1> y;
@@ -479,6 +493,7 @@ struct ScaleLds {
         }
       }
     }
+    wave_fence();
   }
 };
 
@@ -515,9 +530,11 @@ __device__ __forceinline__ void few_rows(const W4GemmArgs& g, uint64_t per_group
   const auto group_of = [&](int b) { return FOLD > 4 ? (int)((uint32_t)b * per_group >> 32) : b * NS; };
   int base = 0;  // first group in LDS
   const auto mul = [&](int b, Block& k) {
+    wave_fence();
 #pragma unroll
     for (int i = 0; i < CH; ++i)
       *reinterpret_cast<u32x4*>(xl + (q4 + 4 * i) * 256 + ((r16 ^ (q4 + 4 * i)) & 15) * 16) = turn<FMT>(k.x[i]);
+    wave_fence();
     Items<NS, SIZE> s[NT];
     Items<NS, 1> z[NT];
     const int at = group_of(b) - base;
