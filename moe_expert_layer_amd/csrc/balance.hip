@@ -541,6 +541,11 @@ int chunk_of(int T) {
   return (int)(c < 32 ? 32 : c > 8192 ? 8192 : c);
 }
 int chunks_of(int T) { return (int)(((long long)T + chunk_of(T) - 1) / chunk_of(T)); }
+// the most chunks that T tokens or fewer make, which is what the workspace holds: 8192 tokens are 256 chunks of 32, 8193 are 249 of 33
+int most_chunks(int T) {
+  const long long n = T <= 256 * 8192 ? ((long long)T + 31) / 32 : ((long long)T + 8191) / 8192;
+  return (int)(T <= 256 * 8192 && n > 256 ? 256 : n);
+}
 
 // The shapes: columns a token's lanes hold.  f(lanes per token, chunks per lane)
 template <int V> struct Int { static constexpr int value = V; };
@@ -563,7 +568,7 @@ struct WorkspaceLayout {
 WorkspaceLayout layout_of(int T, int E, int S) {
   WorkspaceLayout L{};
   if (T <= kSmall) return L;
-  const size_t rows = (size_t)chunks_of(T) + S;
+  const size_t rows = (size_t)most_chunks(T) + S;
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     const size_t o = at;
