@@ -505,7 +505,7 @@ typedef struct {
 } moe_balance_desc;
 
 /* Bytes of workspace moe_balance_loss needs.  Fewer tokens, experts or sequences never need more, so that the
- * size for a program's largest batch serves them all.  Host only; validates the descriptor. */
+ * size for a program's largest batch serves them all; never 0.  Host only; validates the descriptor. */
 moe_status moe_balance_workspace_size(const moe_balance_desc* desc, size_t* bytes);
 
 /* Counts, probability sums and losses.  opt_z NULL: no z (MOE_ERR_UNSUPPORTED when given with

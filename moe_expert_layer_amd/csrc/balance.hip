@@ -567,6 +567,7 @@ struct WorkspaceLayout {
 };
 WorkspaceLayout layout_of(int T, int E, int S) {
   WorkspaceLayout L{};
+  L.total = 256;  // never nothing: an allocator may give NULL for that, which the call refuses
   if (T <= kSmall) return L;
   const size_t rows = (size_t)most_chunks(T) + S;
   size_t at = 0;

@@ -32,3 +32,10 @@ def test_more_experts_or_sequences_need_no_less():
         assert [size(T, E, 3) for E in range(1, 1025)] == sorted(size(T, E, 3) for E in range(1, 1025))
         s = [size(T, 60, S) for S in (1, 2, 3, 100, 65535, 65536)]
         assert s == sorted(s)
+
+
+@pytest.mark.parametrize("T,E,S", [(0, 1, 1), (1, 1, 1), (1, 1024, 65536), (1024, 256, 1)])
+def test_the_size_is_never_zero(T, E, S):
+    """The call wants a workspace, so that what the size asks for has to be something that an allocator gives a pointer to."""
+    n = size(T, E, S)
+    assert n > 0 and n % 256 == 0
