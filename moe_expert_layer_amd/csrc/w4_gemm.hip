@@ -141,7 +141,7 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 }
 
-// N (a power of two) consecutive items of SIZE bytes at any alignment of theirs, as they lie; `have`: the first ones only
+// N (a power of two) consecutive items of SIZE bytes at any alignment of theirs, as they lie
 template <int N, int SIZE>
 struct Items {
   static constexpr int kWords = (N * SIZE + 3) / 4;
@@ -167,17 +167,6 @@ struct Items {
         for (int i = 0; i < kStep; ++i) w[j + i] = v[i];
       }
     }
-  }
-  __device__ __forceinline__ void load(gptr p, int have) {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < have) {
-        if constexpr (SIZE == 4) w[i] = ((const MOE_GLOBAL uint32_t*)p)[i];
-        else if constexpr (SIZE == 2) w[i >> 1] |= (uint32_t)((const MOE_GLOBAL uint16_t*)p)[i] << (16 * (i & 1));
-        else w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
-      }
   }
   __device__ __forceinline__ void load_lds(const uint8_t* p) {
     if constexpr (N * SIZE == 1) w[0] = *p;
