@@ -483,12 +483,14 @@ moe_status moe_mxfp4_gemm(const moe_mxfp4_gemm_desc* desc, const uint8_t* a, con
  *   - A logit of -inf gives probability 0; a token whose logits are all -inf has probabilities 0,
  *     adds 0 to z and has no gradient, but its ids are counted.  NaN (and, with softmax, +inf) makes
  *     its token's probabilities and what they enter NaN.
- *   - Probabilities are float32; sums over tokens run in a fixed order (no atomics in them), partial
- *     sums in float32 over at most 1024 tokens of one lane and its workgroup's others, the rest in float64; the counts' integer sums
- *     do not depend on the order.  The same from run to run.
+ *   - Probabilities are float32, off by up to some (2.3 d + 70) 2^-24 of themselves, d how far the logit lies below
+ *     its token's largest; sums over tokens run in a fixed order (no atomics in them), partial sums in
+ *     float32 over at most 1024 tokens of one lane and its workgroup's others, the rest in float64; the
+ *     counts' integer sums do not depend on the order.  The same from run to run.
  *   - Pointers are aligned to their element; add may be dlogits itself, otherwise outputs must not
  *     overlap inputs or each other.  Stream, validation and error rules are those at the top of this file;
- *     num_tokens = 0 launches nothing and writes nothing.
+ *     num_tokens = 0 launches nothing and writes nothing, no zeros either: a program that sums counts and tokens over
+ *     GPUs, one of which may have no tokens, clears them there itself.
  *   - Limits: 1 <= E_tot <= 1024; 1 <= k <= 16; 1 <= num_seqs <= 65536; T*k <= 2^31 - 2^17; strides 0
  *     (= E_tot) or E_tot to 2^40. */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
@@ -580,8 +582,8 @@ typedef struct {
   int64_t out_stride;     /* elements between rows of C; 0 = N */
 } moe_w4_gemm_desc;
 
-/* Grouped product of 16-bit rows with 4-bit weights for few rows per group (decoding), the weights
- * read once for every 64 rows or fewer:
+/* Grouped product of 16-bit rows with 4-bit weights for few rows per group (decoding).  A group's weights are
+ * read once for every 16 of its rows or, with many rows per group, for every 64 or fewer:
  *   c[r, n] = sum_k a[r, k] * w[e, n, k]   for offsets[e] <= r < offsets[e + 1]
  * or, with an activation, w holding 2N rows per group (gate [0, N), up [N, 2N)), the layer's
  *   c[r, n] = act(sum_k a[r, k] * w[e, n, k], sum_k a[r, k] * w[e, N + n, k])
@@ -590,7 +592,10 @@ typedef struct {
  * (moe_sort_tokens) and cut to [0, rows], or NULL with one group: all rows.  Rows of c in no group
  * are left as they were.  Descending offsets give unspecified results, but no access outside the
  * tensors.  Products are exact, sums float32 in an order that depends on the sizes only, the scale is
- * applied to each group's sum in float32, and the result is rounded once to the type of C.
+ * applied to each group's sum in float32, and the result is rounded once to the type of C.  INT4's zero
+ * point comes off the sums (sum a q - z sum a): beside what the float32 sum over the groups loses, a result is off by up to
+ * (min(G, 128) + 4) 2^-24 of the sum of |a| (q + z) s, not of |a (q - z) s|.  A value of A that is larger than the others by
+ * orders of magnitude thus limits its row's accuracy also where it meets a weight of 0.
  * b 16-byte aligned, the rest to their elements; b_zeros NULL without zero points; c must not
  * overlap the inputs.  No workspace.  Stream, validation and error rules are those at the top of
  * this file; rows = 0 launches nothing. */

@@ -592,7 +592,8 @@ def moe_balance_loss(desc, logits, topk_ids, counts, tokens, prob_sums, balance,
                      seq_offsets=None, stream=None):
     """Counts int32 [S, E_tot], tokens int32 [S], prob_sums [S, E_tot], the balance loss [S] and, where given, the z loss
     [S] of the routing logits [T, E_tot] and the experts chosen, topk_ids int32 [T, k].  mask (bool or uint8 [T]): the
-    tokens that count; seq_offsets int32 [S + 1]: the sequences' tokens (None: one sequence of all tokens)."""
+    tokens that count; seq_offsets int32 [S + 1]: the sequences' tokens (None: one sequence of all tokens).  With no tokens
+    at all (num_tokens 0) nothing is written: clear counts and tokens first where they are summed over GPUs."""
     v, dev = _view(_BalanceView, desc), _device_of(logits)
     v.inputs(logits, mask, seq_offsets, dev)
     _array("topk_ids", topk_ids, v.i32, v.slots, dev)

@@ -15,8 +15,8 @@
 // token would take six steps for one.  Sums over tokens stay in the lanes' registers, over all tokens that a lane sees
 // of a piece (the tokens of one workgroup's chunk in one sequence), then over a wave's groups, then over waves.
 //
-// 65536 tokens of 256 float32 logits: forward 22 us, some 7 of them to join the pieces (14 us at a copy's rate), gradient with another one added
-// to it 39 us (41); 128 tokens of 32: 3.7 us, 6.6 with the launch.
+// 65536 tokens of 256 float32 logits: forward 22 us, some 6.5 of them to join the pieces (14 us at a copy's rate), gradient with another one added
+// to it 39 us (41); 128 tokens of 32: 3.6 us, 6.2 to 6.8 with the call.
 #include <hip/hip_runtime.h>
 #include <cstddef>
 #include <cstdint>
@@ -113,7 +113,9 @@ struct Columns {
 };
 
 // One token's probabilities.  x: logits, -inf in columns that are not this lane's; on return p[r][i] unscaled
-// and 1 / their sum (0 where every logit is -inf).
+// and 1 / their sum (0 where every logit is -inf).  The difference to the largest logit, its product with log2 e and that constant are
+// float32, so an exponential is off by up to some 2.3 |x - m| 2^-24 of itself (1.3 where x - m is exact), which is most for the
+// shares that matter least; a base-2 exponent in two parts would take that off for some four more vector instructions a logit.
 template <int LPT, int R>
 __device__ __forceinline__ float probabilities(const float (&x)[R][4], float (&p)[R][4], bool sigmoid, float& top,
                                                float& sum) {
@@ -532,10 +534,16 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceShape b, c
 }
 
 constexpr int kWaves = 8;     // waves of the forward kernels
-constexpr int kSmall = 1024;  // at most this many tokens: one workgroup a sequence
+// At most this many tokens: one workgroup a sequence, and no second kernel.  One sequence of float32 logits, in one workgroup and in pieces, us:
+// 32 experts, 128 tokens 7.2 and 9.5, 512 7.6 and 9.5, 1024 12.3 and 9.5; 256 experts, 128 tokens 7.8 and 10.8, 256 11.8 and 10.9, 1024 36
+// and 11; 1024 experts, 64 tokens 11.6 and 13, 128 19.5 and 13, 1024 131 and 14.  So one workgroup is the better up to eight rounds of the
+// tokens that it takes at a time (128 with up to 16 experts, 8 above 512), and this border is far past that for many experts in one sequence;
+// with many sequences their workgroups run side by side.
+constexpr int kSmall = 1024;
 
 // Tokens of a workgroup's chunk: for 256 chunks, one for each CU (256, 512, 1024 of them: 22, 24, 29 us for 65536 tokens of 256, the pieces being
-// joined after), but no fewer than a workgroup takes at a time, and no more than leave 1024 to the sums of one lane
+// joined after), but no fewer than 32, which a workgroup takes at a time with 33 to 512 experts (128 with up to 16, 64 with up to 32, where
+// some of its waves then have none, and 8 above), and no more than leave 1024 to the sums of one lane
 int chunk_of(int T) {
   const long long c = ((long long)T + 255) / 256;
   return (int)(c < 32 ? 32 : c > 8192 ? 8192 : c);

@@ -10,7 +10,8 @@
 // Both directions are bound by HBM.  A lane takes 8 values (one or two 16-byte loads) and leaves 4 bytes of codes; 4, 8 or
 // 16 lanes hold a group of 32, 64 or 128.  Larger groups are walked 128 values at a time by 16 lanes, twice, the second
 // time from the caches.  16384 x 7168 float32 values with groups of 128 and zero points, and
-// back to bf16: 163 us for the two, 156 at a copy's rate, values read once and values written going past the caches (182 us through them).
+// back to bf16: 158 to 167 us for the two (109 and 57 traced), 156 at a copy's rate, values read once and values written going past the caches
+// (182 us through them).
 #include <hip/hip_runtime.h>
 #include <cstdint>
 

@@ -15,11 +15,14 @@
 // codes of quarter j, a run of 32.
 //
 // Three kernels: few rows with K split over waves, few rows by many weight rows, and tiles of up to 64 rows (launch has the rule).  With few
-// rows HBM is the bound: 128 rows in 32 experts of 4096 x 7168 take 97 us with groups of 128 and zero points (5.1 TB/s; a copy runs at 4.9), MXFP4
-// weights of 7168 x 2048 61 us (4.2 TB/s: four scales a block of 128 and their sums); one row through 4096 x 7168 7 us, of which a
-// launch is 4.  Tiles are bound by instructions: 2000 rows through 32 experts of 4096 x 4096 with groups of 64 take 174 us, 65 at a
-// copy's rate; of a SIMD's cycles the matrix instructions take 24% and the vector ones 45% (the scaled additions two fifths of
-// those), and two waves a SIMD, all that the registers allow, leave much of the rest empty.
+// rows HBM is the bound: 128 rows in 32 experts of 4096 x 7168 take 95 to 97 us with groups of 128 and zero points (5.1 TB/s; a copy runs at 4.9),
+// MXFP4 weights of 7168 x 2048 61 us (4.2 TB/s: four scales a block of 128 and their sums).  One row through 4096 x 7168 takes 7 us, nearly
+// all of them the kernel's: 3 at a copy's rate, but a workgroup a CU has some 8 KB of loads under way, too few for that.  Tiles are bound by
+// instructions: 2000 rows through 32 experts of 4096 x 4096 with groups of 64 take 164 to 173 us, 65 at a copy's rate; of a SIMD's cycles the
+// matrix instructions take 24% and the vector ones 45% (the scaled additions two fifths of those), and two waves a SIMD, all that the
+// registers allow, leave much of the rest empty.  64 rows in each of those experts: 143 us with groups of 128 or MXFP4 weights, 172 with
+// groups of 64 (4 to 8 vector registers spilled), 455 with groups of 32 (110 to 113: four sets of sums and scales a block live beside the
+// sums over K).  The kernel of many weight rows spills 10 and 27 with float32 scales and groups of 32 and 64.
 #include <hip/hip_runtime.h>
 #include <cstdint>
 
@@ -920,13 +923,18 @@ hipError_t launch(const W4GemmArgs& g, hipStream_t s) {
   const bool act = g.act >= 0;
   // Up to 16 rows an expert the weights are read once either way.  Above, the tile kernel reads them once for 64 rows, but its workgroups are
   // long: with less than one for each CU the few-rows kernel, a round for every 16 rows, is faster up to 64 rows an expert (64 rows through
-  // 8192 x 8192: 41 us and 64; 128 rows: 79 and 64; 24 rows in each of 32 experts of 4096 x 4096: 143 and 110).
+  // 8192 x 8192: 40 us and 64; 128 rows: 79 and 64; 24 rows in each of 32 experts of 4096 x 4096: 143 and 110).
   const long long avg = (g.rows + g.groups - 1) / g.groups, wide = act ? 64 : 128;
   const long long workgroups = g.groups * ((g.N + wide - 1) / wide);
   if (avg > 64 || (avg > 16 && workgroups >= 256)) return go(w4_tile_kernel<XT, FMT, SIZE, FOLD>, (int)wide, 256, kTileRows);
-  // Each wave of the stream kernel reads its own rows' whole length, the few-rows kernel's waves share a row: many rows keep the card
-  // busy with the first (32 experts of 4096 x 7168, 4 rows each: 105 us and 118), fewer with the second (16 experts of 7168 x 2048: 66
-  // and 60; 4096 x 7168 alone: 8.9 and 6.1), which takes 32 weight rows a workgroup or, where that gives too few, 16
+  // Each wave of the stream kernel reads its own rows' whole length, the few-rows kernel's waves share a row: many weight rows keep the
+  // card busy with the first, fewer with the second.  K = 7168, stream and few: 131072 weight rows (32 experts of 4096), 1 row of each expert 66
+  // and 69 us, 4 rows 95 and 109, 16 rows 160 and 178; 114688 (16 of 7168) 65 and 61, 88 and 96, 133 and 145; 100352 (14 of 7168) 60 and
+  // 56, 84 and 85, 129 and 136.  One row of each expert changes sides at some 120000, more rows below 100000: the border suits those.
+  // A workgroup of the few-rows kernel has 32 weight rows or, where that gives too few workgroups, 16.  K = 7168, 32 and 16: 10000
+  // weight rows (2 experts), 1 row 8.5 and 8.2, 4 rows 11.1 and 10.4; 16384 in 8 experts 11.7 and 9.8, 14.4 and 16.9, in one 12.8 and 15.9,
+  // 13.5 and 16.1; 32768 in 16 experts 18.8 and 19.8, 32.7 and 37.1.  One border for all of them is coarse: up to a sixth either way
+  // between 8192 and 16384.
   const long long weight_rows = (long long)g.groups * g.N * (act ? 2 : 1);
   if (weight_rows >= 98304) return go(w4_stream_kernel<XT, FMT, SIZE, FOLD, 2>, (int)wide, 256, 16);
   if (act || weight_rows > 8192) return go(w4_few_kernel<XT, FMT, SIZE, FOLD, 2, 4>, act ? 16 : 32, 256, 16);
